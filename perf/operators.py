@@ -226,7 +226,8 @@ def _codes(x, rand=None):
     top = x.abs().amax(-1)
     zero = top < TINY
     scale = torch.where(zero, 0.0, top / 127.0)
-    r = x.double() * torch.where(zero, 0.0, 127.0 / top.double()).unsqueeze(-1)
+    r = x.double() * 127.0 / torch.where(zero, 1.0, top.double()).unsqueeze(-1)
+    r = torch.where(zero.unsqueeze(-1), 0.0, r)
     if rand is None:
         q = torch.round(r)
     else:                                                        # offset in [0, 1) per element

@@ -299,6 +299,196 @@ SSM_API ssm_status_t ssm_selective_state_update_ex(const ssm_update_args_t* args
 SSM_API ssm_status_t ssm_selective_scan_fwd_noalloc(const ssm_scan_args_t* args,
                                                     ssm_stream_t stream);
 
+/* ------------------------------------------------------------------ training --
+ *
+ * The gradients of the scan and of the conv (the pages describe the forward path only;
+ * these are the adjoints of the formulas above), and activations kept in 8 bits between
+ * the two passes. Conventions as above: nothing is allocated, arguments are checked
+ * before any launch, and the sums over batch, positions and channels are taken in fp32 in
+ * a fixed order, so that a call repeated on the same inputs gives the same bits.
+ */
+
+/* Positions of a channel that share one scale of an 8-bit activation. */
+#define SSM_CHECKPOINT_BLOCK 64
+
+/* Arguments of ssm_selective_scan_bwd. Zero-initialise, then fill. Fields named as in
+ * ssm_scan_args_t mean what they mean there, with the same layouts and strides. */
+typedef struct {
+    ssm_dtype_t dtype;        /* element type of u, delta, z, B, C, dout and their gradients */
+    int64_t batch, dim, seqlen;
+    int64_t dstate;           /* 1..SSM_MAX_SCAN_DSTATE */
+    const void* u;            /* the forward call's u (its pre-conv x with conv_weight) */
+    const void* delta;
+    const float* A;
+    const void* B;
+    const void* C;
+    const float* D;           /* or NULL */
+    const void* z;            /* or NULL */
+    const float* delta_bias;  /* or NULL */
+    int32_t delta_softplus, reverse;
+    const float* conv_weight; /* or NULL */
+    const float* conv_bias;   /* or NULL */
+    int32_t conv_width;
+    const float* initial_state; /* or NULL; forward scans only */
+    const void* conv_history; /* or NULL; forward scans with conv_weight only */
+    const int32_t* seq_starts; /* or NULL; packed sequences: as in the forward call, and
+                                 without dfinal_state */
+    int32_t num_seqs;
+    int32_t channel_last;
+    int64_t stride_u, stride_delta, stride_z, stride_B, stride_C;
+    int32_t a_heads;
+    /* Activations kept in 8 bits (ssm_checkpoint_pack): with u_scale set, u, delta and z
+     * (where given) are int8 codes in the activations' layout and u_scale, delta_scale,
+     * z_scale their scales. Every gradient is that of the values read back. */
+    const float *u_scale, *delta_scale, *z_scale;
+    /* gradients that come in */
+    const void* dout;         /* gradient of the forward call's out, same layout */
+    int64_t stride_dout;      /* channel-last: as the other strides */
+    const float* dfinal_state; /* (batch, dim, dstate) gradient of final_state, or NULL */
+    /* gradients that go out; the optional ones may be NULL */
+    void* du;                 /* of u (of the pre-conv x with conv_weight) */
+    void* ddelta;
+    float* dA;                /* shaped as A */
+    void* dB;
+    void* dC;
+    float* dD;                /* (dim), optional */
+    void* dz;                 /* optional; needs z */
+    float* ddelta_bias;       /* (dim), optional */
+    float* dconv_weight;      /* (dim, conv_width), optional; needs conv_weight */
+    float* dconv_bias;        /* (dim), optional; needs conv_weight */
+    float* dinitial_state;    /* (batch, dim, dstate), optional; forward scans only */
+    void* dconv_history;      /* (batch, dim, conv_width - 1), optional; needs conv_history */
+    int64_t stride_du, stride_ddelta, stride_dz, stride_dB, stride_dC; /* channel-last */
+    void* workspace;          /* device scratch, >= ssm_selective_scan_bwd_workspace_size */
+    size_t workspace_bytes;
+    int32_t num_segments;     /* 0 = automatic; 1 = one sweep per row; k > 1 = the sequence
+                                 in about k segments that run at the same time, for batches
+                                 too narrow to fill the GPU (one more pass over the inputs).
+                                 The results agree within rounding. */
+} ssm_scan_bwd_args_t;
+
+/* Bytes of device workspace the call with these arguments needs. Pointers are only
+ * compared with NULL. The larger part holds the states before every 8th step: about
+ * batch * dim * seqlen * dstate / 2 bytes. */
+SSM_API ssm_status_t ssm_selective_scan_bwd_workspace_size(const ssm_scan_bwd_args_t* args,
+                                                           size_t* bytes);
+
+/*
+ * Gradients of ssm_selective_scan_fwd with respect to all its inputs, from those inputs
+ * alone (nothing of the forward call is kept but them). Covers what the forward call
+ * covers with input-dependent B and C in one direction: either layout, the fused conv,
+ * the reverse direction, a continued sequence, packed sequences, A per head, d_state up
+ * to 128. The gradient of the bidirectional sum is the sum of two calls, one per
+ * direction. No output may overlap an input or another output, element for element
+ * (views of one tensor, such as du and dz in the halves of an in_proj gradient, are fine).
+ * Errors: as the forward call's; SSM_ERR_UNSUPPORTED also for dfinal_state with
+ * seq_starts, and for initial_state, conv_history, dinitial_state with reverse;
+ * SSM_ERR_NULL_ARG for an output whose input is missing, and for u_scale without
+ * delta_scale (or, with z, z_scale) or the other way round.
+ */
+SSM_API ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* args, ssm_stream_t stream);
+
+/* Bytes of device workspace ssm_causal_conv1d_bwd needs. */
+SSM_API ssm_status_t ssm_causal_conv1d_bwd_workspace_size(int64_t batch, int64_t dim,
+                                                          int64_t seqlen, size_t* bytes);
+
+/*
+ * Gradients of ssm_causal_conv1d_fwd: dx (batch, dim, seqlen) in dtype, dw (dim, width)
+ * and dbias (dim) fp32 (either of the two may be NULL), from its inputs and dout (batch,
+ * dim, seqlen) in dtype. dx must not overlap x or dout (SSM_ERR_ALIAS).
+ */
+SSM_API ssm_status_t ssm_causal_conv1d_bwd(const void* dout, const void* x, const float* w,
+                                           const float* bias, void* dx, float* dw, float* dbias,
+                                           int64_t batch, int64_t dim, int64_t seqlen,
+                                           int32_t width, int32_t apply_silu, ssm_dtype_t dtype,
+                                           void* workspace, size_t workspace_bytes,
+                                           ssm_stream_t stream);
+
+/*
+ * Packs an activation into 8 bits for the time between the forward and the backward pass.
+ * x: (batch, dim, seqlen) in dtype, or channel-last (batch, seqlen, dim) with stride_x
+ * elements between positions (0 = dense). codes: int8 of the same shape, dense. scales:
+ * fp32 (batch, dim, nb), or channel-last (batch, nb, dim), nb = ceil(seqlen / 64).
+ * Over each 64 consecutive positions of a channel (fewer at the end) scale = max|x| / 127
+ * and code = round(127 x / max|x|), ties to even, so that code * scale is within half a
+ * step (max|x| / 254) of x. A block whose max|x| is below 2^-100 becomes zeros; one that
+ * holds an infinity or a NaN reads back as NaN throughout.
+ */
+SSM_API ssm_status_t ssm_checkpoint_pack(const void* x, void* codes, float* scales, int64_t batch,
+                                         int64_t dim, int64_t seqlen, int32_t channel_last,
+                                         int64_t stride_x, ssm_dtype_t dtype, ssm_stream_t stream);
+
+/* Reads a packed activation back: out (dense, laid out as the codes) = code * scale in
+ * fp32, rounded once to dtype. */
+SSM_API ssm_status_t ssm_checkpoint_unpack(const void* codes, const float* scales, void* out,
+                                           int64_t batch, int64_t dim, int64_t seqlen,
+                                           int32_t channel_last, ssm_dtype_t dtype,
+                                           ssm_stream_t stream);
+
+/* ------------------------------------------------------- 8-bit decode states --
+ *
+ * A cache of decode states in 8 bits: num_slots slots of (dim, dstate) int8 codes, and one
+ * fp32 scale per (slot, channel). The row of a channel's states is held as codes
+ * round(127 h / max|h|), ties to even, and scale max|h| / 127; a row whose max|h| is below
+ * 2^-100 becomes zeros, one that holds an infinity or a NaN reads back as NaN.
+ *
+ * slots: device int32 (batch): the slot of each batch row, or NULL (row i uses slot i). A
+ * row whose slot is outside [0, num_slots) is padding: it is skipped, nothing of it is
+ * read, and its outputs are left as they were. Two rows of one call must not name the same
+ * slot in a call that writes the cache (the slot then holds a mix of the two rows).
+ *
+ * rand: device uint32 (batch, dim), or NULL. With it a row is rounded to one of the two
+ * neighbouring codes at random instead of to the nearest: state n gets
+ * floor(127 h / max|h| + x_n), x_n the top 24 bits of (rand + n * 0x9E3779B9) mod 2^32 as a
+ * fraction. Over random bits the stored value is right on average, so that a state that
+ * decays by less than half a step per token still decays.
+ */
+typedef struct {
+    ssm_dtype_t dtype;
+    int64_t batch, dim;
+    int64_t dstate;           /* 1..SSM_MAX_SCAN_DSTATE */
+    int64_t num_slots;
+    void* codes;              /* (num_slots, dim, dstate) int8, in/out */
+    float* scales;            /* (num_slots, dim), in/out */
+    const int32_t* slots;     /* (batch) or NULL */
+    const uint32_t* rand;     /* (batch, dim) or NULL */
+    void* conv_state;         /* (num_slots, dim, conv_width) in dtype, in/out; or NULL */
+    const void* x;            /* (batch, dim), as the fields below */
+    const void* dt;
+    const float* A;           /* (dim, dstate), or (a_heads) with a_heads > 0 */
+    const void* B_t;          /* (batch, dstate) */
+    const void* C_t;          /* (batch, dstate) */
+    const float* D;           /* (dim) or NULL */
+    const void* z;            /* (batch, dim) or NULL */
+    const float* dt_bias;     /* (dim) or NULL */
+    int32_t dt_softplus;
+    const float* conv_weight; /* (dim, conv_width) or NULL */
+    const float* conv_bias;   /* (dim) or NULL */
+    int32_t conv_width;
+    void* out;                /* (batch, dim) */
+    int32_t a_heads;
+} ssm_cached_update_args_t;
+
+/* The decode step of ssm_selective_state_update_ex on a cache: reads the row's state from
+ * its slot, takes one step in fp32, gives out from the new state before it is rounded, and
+ * writes the state back in 8 bits. conv_state is held per slot too. Errors as there;
+ * SSM_ERR_BAD_SHAPE also for num_slots < batch without slots. */
+SSM_API ssm_status_t ssm_selective_state_update_cached(const ssm_cached_update_args_t* args,
+                                                       ssm_stream_t stream);
+
+/* Writes fp32 states (batch, dim, dstate) into their slots. */
+SSM_API ssm_status_t ssm_state_cache_write(const float* state, void* codes, float* scales,
+                                           const int32_t* slots, const uint32_t* rand,
+                                           int64_t batch, int64_t dim, int64_t dstate,
+                                           int64_t num_slots, ssm_stream_t stream);
+
+/* Reads the rows' states back: out (batch, dim, dstate) in dtype = code * scale in fp32,
+ * rounded once. */
+SSM_API ssm_status_t ssm_state_cache_read(const void* codes, const float* scales,
+                                          const int32_t* slots, void* out, int64_t batch,
+                                          int64_t dim, int64_t dstate, int64_t num_slots,
+                                          ssm_dtype_t dtype, ssm_stream_t stream);
+
 /* Read and clear the device-side error word (0 = none; 1 = a bounded wait ran out).
  * Synchronises `stream`. */
 SSM_API ssm_status_t ssm_device_error(int32_t* code, ssm_stream_t stream);

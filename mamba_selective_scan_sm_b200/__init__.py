@@ -11,6 +11,10 @@ Functions carry the ABI's names:
 * ``ssm_causal_conv1d_fwd(x, w, bias=None, apply_silu=True)``
 * ``ssm_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, ...)``
 * ``ssm_selective_state_update(state, conv_state, x, dt, A, B, C, ...)`` (in place)
+
+Training (``training.py``): ``ssm_selective_scan_bwd``, ``ssm_causal_conv1d_bwd``,
+``ssm_checkpoint_pack`` / ``ssm_checkpoint_unpack``. Decode states in 8 bits (``cache.py``):
+``ssm_state_cache_write`` / ``ssm_state_cache_read``, ``ssm_selective_state_update_cached``.
 """
 from __future__ import annotations
 
@@ -20,7 +24,11 @@ from . import _abi
 from ._abi import LibraryMissing, SSMError, ScanArgs  # noqa: F401
 
 __all__ = ["ssm_causal_conv1d_fwd", "ssm_selective_scan_fwd", "ssm_selective_scan_workspace_size",
-           "ssm_selective_state_update", "ssm_device_error", "LibraryMissing", "SSMError", "ssm_wait_selftest"]
+           "ssm_selective_state_update", "ssm_device_error", "LibraryMissing", "SSMError", "ssm_wait_selftest",
+           "ssm_selective_scan_bwd", "ssm_selective_scan_bwd_workspace_size", "ScanGrads",
+           "ssm_causal_conv1d_bwd", "ConvGrads", "ssm_checkpoint_pack", "ssm_checkpoint_unpack",
+           "Packed8", "ssm_state_cache_write", "ssm_state_cache_read",
+           "ssm_selective_state_update_cached"]
 
 
 def _torch():
@@ -279,3 +287,22 @@ def ssm_wait_selftest(limit_ns=1_000_000, stream=None) -> None:
     ``limit_ns`` and sets the device error word (read it with ssm_device_error)."""
     lib = _abi.load()
     _abi.check(lib, lib.ssm_wait_selftest(int(limit_ns), _stream(stream)))
+
+
+
+_TRAINING = ("ssm_selective_scan_bwd", "ssm_selective_scan_bwd_workspace_size", "ScanGrads",
+             "ssm_causal_conv1d_bwd", "ConvGrads", "ssm_checkpoint_pack", "ssm_checkpoint_unpack",
+             "Packed8")
+_CACHE = ("ssm_state_cache_write", "ssm_state_cache_read", "ssm_selective_state_update_cached")
+
+
+def __getattr__(name):
+    # the training and cache bindings import torch, which this module leaves to first use
+    if name in _TRAINING:
+        from . import training as module
+    elif name in _CACHE:
+        from . import cache as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(module, name)
+    return value

@@ -20,7 +20,10 @@ EXPORTS = (
     "ssm_abi_version", "ssm_status_string", "ssm_last_error_detail", "ssm_causal_conv1d_fwd",
     "ssm_selective_scan_workspace_size", "ssm_selective_scan_fwd", "ssm_selective_state_update",
     "ssm_selective_state_update_ex", "ssm_device_error", "ssm_selective_scan_fwd_noalloc",
-    "ssm_wait_selftest",
+    "ssm_wait_selftest", "ssm_selective_scan_bwd_workspace_size", "ssm_selective_scan_bwd",
+    "ssm_causal_conv1d_bwd_workspace_size", "ssm_causal_conv1d_bwd", "ssm_checkpoint_pack",
+    "ssm_checkpoint_unpack", "ssm_selective_state_update_cached", "ssm_state_cache_write",
+    "ssm_state_cache_read",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 ABI_VERSION = 4            # SSM_ABI_VERSION of include/ssm.h this mirror follows
@@ -60,6 +63,39 @@ class UpdateArgs(ctypes.Structure):
         ("C_t", _P), ("D", _P), ("z", _P), ("dt_bias", _P), ("dt_softplus", _I32),
         ("conv_weight", _P), ("conv_bias", _P), ("conv_width", _I32), ("out", _P),
         ("a_heads", _I32),
+    ]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    """Mirror of ssm_scan_bwd_args_t (field order and types as in include/ssm.h)."""
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("batch", _I64), ("dim", _I64), ("seqlen", _I64), ("dstate", _I64),
+        ("u", _P), ("delta", _P), ("A", _P), ("B", _P), ("C", _P), ("D", _P), ("z", _P),
+        ("delta_bias", _P), ("delta_softplus", _I32), ("reverse", _I32),
+        ("conv_weight", _P), ("conv_bias", _P), ("conv_width", _I32),
+        ("initial_state", _P), ("conv_history", _P), ("seq_starts", _P), ("num_seqs", _I32),
+        ("channel_last", _I32), ("stride_u", _I64), ("stride_delta", _I64), ("stride_z", _I64),
+        ("stride_B", _I64), ("stride_C", _I64), ("a_heads", _I32),
+        ("u_scale", _P), ("delta_scale", _P), ("z_scale", _P),
+        ("dout", _P), ("stride_dout", _I64), ("dfinal_state", _P),
+        ("du", _P), ("ddelta", _P), ("dA", _P), ("dB", _P), ("dC", _P), ("dD", _P), ("dz", _P),
+        ("ddelta_bias", _P), ("dconv_weight", _P), ("dconv_bias", _P), ("dinitial_state", _P),
+        ("dconv_history", _P), ("stride_du", _I64), ("stride_ddelta", _I64), ("stride_dz", _I64),
+        ("stride_dB", _I64), ("stride_dC", _I64),
+        ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("num_segments", _I32),
+    ]
+
+
+class CachedUpdateArgs(ctypes.Structure):
+    """Mirror of ssm_cached_update_args_t (field order and types as in include/ssm.h)."""
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("batch", _I64), ("dim", _I64), ("dstate", _I64), ("num_slots", _I64),
+        ("codes", _P), ("scales", _P), ("slots", _P), ("rand", _P), ("conv_state", _P),
+        ("x", _P), ("dt", _P), ("A", _P), ("B_t", _P), ("C_t", _P), ("D", _P), ("z", _P),
+        ("dt_bias", _P), ("dt_softplus", _I32), ("conv_weight", _P), ("conv_bias", _P),
+        ("conv_width", _I32), ("out", _P), ("a_heads", _I32),
     ]
 
 
@@ -105,6 +141,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.ssm_device_error.argtypes = [ctypes.POINTER(_I32), _P]
     lib.ssm_wait_selftest.restype = ctypes.c_int
     lib.ssm_wait_selftest.argtypes = [ctypes.c_uint64, _P]
+    lib.ssm_selective_scan_bwd_workspace_size.restype = ctypes.c_int
+    lib.ssm_selective_scan_bwd_workspace_size.argtypes = [ctypes.POINTER(ScanBwdArgs),
+                                                          ctypes.POINTER(ctypes.c_size_t)]
+    lib.ssm_selective_scan_bwd.restype = ctypes.c_int
+    lib.ssm_selective_scan_bwd.argtypes = [ctypes.POINTER(ScanBwdArgs), _P]
+    lib.ssm_causal_conv1d_bwd_workspace_size.restype = ctypes.c_int
+    lib.ssm_causal_conv1d_bwd_workspace_size.argtypes = [_I64, _I64, _I64,
+                                                         ctypes.POINTER(ctypes.c_size_t)]
+    lib.ssm_causal_conv1d_bwd.restype = ctypes.c_int
+    lib.ssm_causal_conv1d_bwd.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32,
+                                          ctypes.c_int, _P, ctypes.c_size_t, _P]
+    lib.ssm_checkpoint_pack.restype = ctypes.c_int
+    lib.ssm_checkpoint_pack.argtypes = [_P, _P, _P, _I64, _I64, _I64, _I32, _I64, ctypes.c_int, _P]
+    lib.ssm_checkpoint_unpack.restype = ctypes.c_int
+    lib.ssm_checkpoint_unpack.argtypes = [_P, _P, _P, _I64, _I64, _I64, _I32, ctypes.c_int, _P]
+    lib.ssm_selective_state_update_cached.restype = ctypes.c_int
+    lib.ssm_selective_state_update_cached.argtypes = [ctypes.POINTER(CachedUpdateArgs), _P]
+    lib.ssm_state_cache_write.restype = ctypes.c_int
+    lib.ssm_state_cache_write.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]
+    lib.ssm_state_cache_read.restype = ctypes.c_int
+    lib.ssm_state_cache_read.argtypes = [_P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int, _P]
     if lib.ssm_abi_version() != ABI_VERSION:
         raise LibraryMissing(f"{path} implements ABI {lib.ssm_abi_version()}, this binding "
                              f"expects {ABI_VERSION}: rebuild the library")

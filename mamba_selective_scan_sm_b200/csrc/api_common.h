@@ -1,0 +1,69 @@
+// Argument checks shared by the host code of the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "../../include/ssm.h"
+#include "launch.h"
+
+namespace ssm {
+
+inline ssm_status_t api_fail(ssm_status_t s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    set_error_detail(buf);
+    return s;
+}
+
+inline ssm_status_t api_ok() {
+    set_error_detail("");
+    return SSM_OK;
+}
+
+inline ssm_status_t api_cuda(cudaError_t e, const char* what) {
+    return api_fail(SSM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// A pointer argument: its alignment, and the bytes it spans (0 where they are not checked).
+struct Arg {
+    const void* p;
+    size_t align, bytes;
+    const char* name;
+};
+
+template <int N>
+inline ssm_status_t check_aligned(const Arg (&args)[N]) {
+    for (const Arg& a : args)
+        if (a.p && !is_aligned(a.p, a.align))
+            return api_fail(SSM_ERR_MISALIGNED, "%s is not %zu-byte aligned", a.name, a.align);
+    return SSM_OK;
+}
+
+template <int NO, int NI>
+inline ssm_status_t check_alias(const Arg (&outs)[NO], const Arg (&ins)[NI]) {
+    for (const Arg& o : outs)
+        for (const Arg& i : ins)
+            if (ranges_overlap(o.p, o.bytes, i.p, i.bytes))
+                return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", o.name, i.name);
+    return SSM_OK;
+}
+
+inline bool bad_dtype(ssm_dtype_t t) { return t != SSM_F32 && t != SSM_BF16; }
+inline int size_of(ssm_dtype_t t) { return t == SSM_BF16 ? 2 : 4; }
+
+}  // namespace ssm

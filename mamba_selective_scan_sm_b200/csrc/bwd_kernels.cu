@@ -1,0 +1,163 @@
+// The backward pass's small kernels (carry chain, reductions, sequence starts) and the
+// conv's gradient.
+#define SSM_ERROR_WORD g_error_bwd
+#include "conv_bwd_kernel.cuh"
+
+#include "bwd_launch.h"
+
+namespace ssm {
+
+// min(position - start of its sequence, 4) for every position of a packed row, from the
+// offsets (a binary search per position; offsets out of order or range give some value in
+// 0..4, never an access outside).
+__global__ void __launch_bounds__(256) since_kernel(const int32_t* cu, int nseq, int seqlen, uint8_t* out) {
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t >= seqlen) return;
+    int lo = 0, hi = nseq;                                     // last s in [0, nseq) with cu[s] <= t
+    while (hi - lo > 1) {
+        const int m = lo + (hi - lo) / 2;
+        if (cu[m] <= t) lo = m;
+        else hi = m;
+    }
+    const int64_t d = (int64_t)t - cu[lo];
+    out[t] = (uint8_t)(d < 0 ? 0 : d > 4 ? 4 : d);
+}
+
+// dB and dC: the sum over the channel groups of their partial rows, rounded once. A CTA
+// takes kReduceSteps steps of one batch row; the sums pass through shared memory, since
+// (batch, dstate, seqlen) outputs run along the steps and the partial rows along the states.
+constexpr int kReduceSteps = 16;
+template <typename T>
+__global__ void __launch_bounds__(256) scan_bwd_reduce_bc_kernel(const BwdReduceParams p) {
+    extern __shared__ float sm[];
+    const int row = 2 * p.ns, b = blockIdx.y, t0 = blockIdx.x * kReduceSteps;
+    const int nt = min(kReduceSteps, p.seqlen - t0);
+    const int64_t gstride = (int64_t)p.batch * p.seqlen * row;
+    const float* src = p.parts + ((int64_t)b * p.seqlen + t0) * row;
+    for (int k = threadIdx.x; k < nt * row; k += blockDim.x) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int g = 0; g < p.groups; ++g) v += src[g * gstride + k];
+        sm[(k / row) * (row + 1) + k % row] = v;
+    }
+    __syncthreads();
+    const bool along_p = p.sdB.p == 1 && p.sdB.c != 1;
+    for (int k = threadIdx.x; k < nt * p.dstate * 2; k += blockDim.x) {
+        const int which = k / (nt * p.dstate), r = k % (nt * p.dstate);
+        const int n = along_p ? r / nt : r % p.dstate, tl = along_p ? r % nt : r / p.dstate;
+        const int pos = p.reverse ? p.seqlen - 1 - (t0 + tl) : t0 + tl;
+        const Str& s = which ? p.sdC : p.sdB;
+        T* o = static_cast<T*>(which ? p.dC : p.dB);
+        o[(int64_t)b * s.b + (int64_t)n * s.c + (int64_t)pos * s.p] =
+            Elem<T>::from_f(sm[tl * (row + 1) + which * p.ns + n]);
+    }
+}
+
+// dA, dD and d delta_bias: sums over the batch rows and segments. A per state: a thread
+// per (channel, state) and per channel. A per head: a CTA per head sums over its channels
+// and states too.
+__global__ void __launch_bounds__(256) scan_bwd_reduce_a_kernel(const BwdReduceParams p) {
+    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t na = p.head_dim ? 0 : (int64_t)p.dim * p.ns;
+    if (idx < na) {
+        const int d = (int)(idx / p.ns), n = (int)(idx % p.ns);
+        if (n >= p.dstate) return;
+        float v = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < p.nrows; ++r) v += p.pA[r * na + idx];
+        p.dA[(int64_t)d * p.dstate + n] = v;
+    } else if (idx < na + 2 * (int64_t)p.dim) {
+        const int64_t k = idx - na;
+        float* o = k % 2 ? p.dbias : p.dD;
+        if (!o) return;
+        float v = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < p.nrows; ++r) v += p.pD[(int64_t)r * p.dim * 2 + k];
+        o[k / 2] = v;
+    }
+}
+
+__global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdReduceParams p) {
+    const int h = blockIdx.x;
+    const int64_t per = (int64_t)p.head_dim * p.ns, first = h * per;
+    float v = 0.f;
+    for (int r = 0; r < p.nrows; ++r) {
+        const float* src = p.pA + (int64_t)r * p.dim * p.ns + first;
+#pragma unroll 4
+        for (int64_t k = threadIdx.x; k < per; k += blockDim.x) v += src[k];
+    }
+    __shared__ float red[256 / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = 0.f;
+        for (int k = 0; k < 256 / 32; ++k) v += red[k];
+        p.dA[h] = v;
+    }
+}
+
+BwdVariant scan_bwd_variant(int lanes) {
+#define SSM_BWD(S_) if (lanes == S_) return {BwdShape<S_>::NS, BwdShape<S_>::G, BwdShape<S_>::TT};
+    SSM_BWD(1) SSM_BWD(2) SSM_BWD(4) SSM_BWD(8) SSM_BWD(16)
+#undef SSM_BWD
+    return {BwdShape<32>::NS, BwdShape<32>::G, BwdShape<32>::TT};
+}
+
+cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st) {
+    const int64_t n = (int64_t)p.batch * p.dim * ns;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+#define SSM_BWD(NS_)                                                                          \
+    if (ns == NS_) {                                                                          \
+        scan_bwd_carry_kernel<NS_><<<blocks, 256, 0, st>>>(p);                                \
+        return cudaGetLastError();                                                            \
+    }
+    SSM_BWD(4) SSM_BWD(8) SSM_BWD(16) SSM_BWD(32) SSM_BWD(64) SSM_BWD(128)
+#undef SSM_BWD
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_scan_bwd_reduce(int elem_size, const BwdReduceParams& p, cudaStream_t st) {
+    const dim3 g((p.seqlen + kReduceSteps - 1) / kReduceSteps, p.batch);
+    const int smem = kReduceSteps * (2 * p.ns + 1) * (int)sizeof(float);
+    if (elem_size == 2) scan_bwd_reduce_bc_kernel<__nv_bfloat16><<<g, 256, smem, st>>>(p);
+    else scan_bwd_reduce_bc_kernel<float><<<g, 256, smem, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t n = (p.head_dim ? 0 : (int64_t)p.dim * p.ns) + 2 * (int64_t)p.dim;
+    scan_bwd_reduce_a_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !p.head_dim) return e;
+    scan_bwd_reduce_heads_kernel<<<p.dim / p.head_dim, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_since(const int32_t* cu, int nseq, int seqlen, uint8_t* since, cudaStream_t st) {
+    since_kernel<<<(seqlen + 255) / 256, 256, 0, st>>>(cu, nseq, seqlen, since);
+    return cudaGetLastError();
+}
+
+int conv_bwd_chunk(bool channel_last) { return channel_last ? kConvClChunk : kConvRowChunk; }
+
+cudaError_t launch_conv_bwd(int elem_size, bool channel_last, const ConvBwdParams& p, cudaStream_t st) {
+    if (channel_last) {
+        const int per = 128 * kConvClRun;
+        const dim3 g((p.dim + per - 1) / per, p.batch, p.chunks);
+        if (elem_size == 2) conv_bwd_cl_kernel<__nv_bfloat16><<<g, 128, 0, st>>>(p);
+        else conv_bwd_cl_kernel<float><<<g, 128, 0, st>>>(p);
+    } else {
+        const int64_t rows = (int64_t)p.batch * p.dim;
+        const dim3 g(p.chunks, (unsigned)(rows < 65535 ? rows : 65535), (unsigned)((rows + 65534) / 65535));
+        if (elem_size == 2) conv_bwd_row_kernel<__nv_bfloat16><<<g, kConvRowThreads, 0, st>>>(p);
+        else conv_bwd_row_kernel<float><<<g, kConvRowThreads, 0, st>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_conv_reduce(const ConvReduceParams& p, cudaStream_t st) {
+    conv_reduce_kernel<<<(unsigned)(((int64_t)p.dim * 5 + 127) / 128), 128, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace ssm

@@ -251,6 +251,20 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     p.softplus = a->delta_softplus ? 1 : 0;
     p.reverse = a->reverse ? 1 : 0;
     p.head_dim = a->a_heads > 0 ? (int)(D / a->a_heads) : 0;
+    // Asynchronous copies take 16 bytes (8 of 8-bit rows in 8-step tiles) of a row at a time,
+    // from tile boundaries counted from either end of the row: bases aligned to 16 bytes, rows
+    // of a multiple of 16 bytes (8-bit rows along the positions: of 16 codes, which every
+    // boundary is a multiple of too).
+    const int64_t unit = 16 / es, unit_in = 16 / ein;
+    bool async = is_aligned(a->u, 16) && is_aligned(a->delta, 16) && is_aligned(a->z, 16) &&
+                 is_aligned(a->B, 16) && is_aligned(a->C, 16) && is_aligned(a->dout, 16);
+    if (cl)
+        async = async && p.x.s.p % unit_in == 0 && p.dt.s.p % unit_in == 0 &&
+                (!a->z || p.z.s.p % unit_in == 0) && p.sdy.p % unit == 0 && p.sB.p % unit == 0 &&
+                p.sC.p % unit == 0;
+    else
+        async = async && L % unit == 0 && L % unit_in == 0;
+    p.async = async ? 1 : 0;
     p.h0 = a->initial_state;
     p.dhl = a->dfinal_state;
     p.hist = a->conv_weight ? a->conv_history : nullptr;
@@ -303,6 +317,7 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     r.nrows = (int)(pl.nseg * Bn);
     r.reverse = p.reverse;
     r.head_dim = p.head_dim;
+    r.order_mask = pl.v.order_mask;
     r.parts = p.parts;
     r.pA = p.pA;
     r.pD = p.pD;

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_a_kernel(const BwdReduceP
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t na = p.head_dim ? 0 : (int64_t)p.dim * p.ns;
     if (idx < na) {
-        const int d = (int)(idx / p.ns), n = (int)(idx % p.ns);
+        const int d = (int)(idx / p.ns), n = (int)(idx % p.ns) ^ (d & p.order_mask);
         if (n >= p.dstate) return;
         float v = 0.f;
 #pragma unroll 8
@@ -99,21 +99,21 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdRed
 }
 
 BwdVariant scan_bwd_variant(int lanes) {
-#define SSM_BWD(S_) if (lanes == S_) return {BwdShape<S_>::NS, BwdShape<S_>::G, BwdShape<S_>::TT};
+#define SSM_BWD(S_) if (lanes == S_) return {BwdShape<S_>::NS, BwdShape<S_>::G, BwdShape<S_>::TT, BwdShape<S_>::NC - 1};
     SSM_BWD(1) SSM_BWD(2) SSM_BWD(4) SSM_BWD(8) SSM_BWD(16)
 #undef SSM_BWD
-    return {BwdShape<32>::NS, BwdShape<32>::G, BwdShape<32>::TT};
+    return {BwdShape<32>::NS, BwdShape<32>::G, BwdShape<32>::TT, BwdShape<32>::NC - 1};
 }
 
 cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st) {
     const int64_t n = (int64_t)p.batch * p.dim * ns;
     const unsigned blocks = (unsigned)((n + 255) / 256);
-#define SSM_BWD(NS_)                                                                          \
-    if (ns == NS_) {                                                                          \
-        scan_bwd_carry_kernel<NS_><<<blocks, 256, 0, st>>>(p);                                \
+#define SSM_BWD(S_)                                                                           \
+    if (ns == 4 * S_) {                                                                       \
+        scan_bwd_carry_kernel<S_><<<blocks, 256, 0, st>>>(p);                                \
         return cudaGetLastError();                                                            \
     }
-    SSM_BWD(4) SSM_BWD(8) SSM_BWD(16) SSM_BWD(32) SSM_BWD(64) SSM_BWD(128)
+    SSM_BWD(1) SSM_BWD(2) SSM_BWD(4) SSM_BWD(8) SSM_BWD(16) SSM_BWD(32)
 #undef SSM_BWD
     return cudaErrorInvalidValue;
 }

@@ -31,6 +31,7 @@ struct BwdParams {
     const float* A;               // (dim, dstate), or (dim / head_dim)
     const float *D, *dbias, *conv_w, *conv_b;
     int conv_width, softplus, reverse, head_dim;
+    int async;                    // every row is aligned to the asynchronous copies' unit
     const float* h0;              // (batch, dim, dstate) or null
     const float* dhl;             // (batch, dim, dstate) or null: gradient of the last state
     const void* hist;             // (batch, dim, conv_width - 1) or null
@@ -69,7 +70,7 @@ struct ConvBwdParams {
 
 // Sums the partial results of a backward pass.
 struct BwdReduceParams {
-    int batch, dim, seqlen, dstate, ns, groups, nrows, reverse, head_dim;
+    int batch, dim, seqlen, dstate, ns, groups, nrows, reverse, head_dim, order_mask;
     const float *parts, *pA, *pD;
     void *dB, *dC;                // in the activations' type
     Str sdB, sdC;

@@ -44,20 +44,56 @@ template <int S> struct BwdShape {
     static constexpr int NS = 4 * S;                           // states, padded
     static constexpr int CW = 32 / S;                          // channels per warp and slot
     static constexpr int KC = S <= 4 ? 1 : S / 4;              // channel slots per warp
+    static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
     static constexpr int G = kBwdWarps * CW * KC;              // channels per CTA
-    static constexpr int TT = S == 4 ? 32 : (S == 2 || S == 8) ? 16 : 8;   // steps per tile
+    static constexpr int TT = S == 1 || S >= 16 ? 8 : 16;      // steps per tile
     static constexpr int NSUB = TT / kSubSteps;
     static constexpr int EPT = G * TT / kBwdThreads;           // elements per thread and tensor
     static constexpr int RB = NS + 4;                          // row of B / C in floats
     // shared memory, in floats
-    static constexpr int kSt = 4 * G * (TT + 1);               // {delta, delta u, g, start}
+    static constexpr int kSt = 4 * G * (TT + 1);               // {delta, delta, delta u, delta u}
+    static constexpr int kG = 2 * G * (TT + 1);                // {g, g}
     static constexpr int kU = G * (TT + 1);
     static constexpr int kOut = G * (TT + 2);                  // one of y, s1, s2
-    static constexpr int kBC = TT * RB;
+    static constexpr int kBC = NC * TT * RB;
     static constexpr int kPart = kBwdWarps * TT * 2 * NS;
     static constexpr int kPrm = 8 * G;
+    static constexpr int kMask = 4;                            // sequence starts of the tile, as bits
     static constexpr int kSum = 2 * G * TT;                    // channel-last dD, dbias sums
     static constexpr int kCarry = KC > 2 ? kBwdThreads * KC * 8 : 0;
+};
+
+// The order of a lane's 4 states. Slot k of a channel's lane j holds state 4 j + (k ^ q),
+// q = the low bits of the channel's place in its warp. Two lanes whose channels differ in
+// bit 1 of q then hold each other's second pair of states in their first pair of slots, and
+// two that differ in bit 0 each other's odd state in the even slot: the sums over a warp's
+// channels exchange the same slots in every lane, without a select per value (measured with
+// the selects: 33 instructions per channel, step and state; without: see scan_bwd_kernel).
+// Everything the kernels pass to one another in scratch memory is in this order.
+template <int S>
+__device__ __forceinline__ int slot_order(int d) {
+    return d & (BwdShape<S>::NC - 1);                          // CTAs begin at multiples of 32 / S
+}
+
+// One tile's inputs as they lie in global memory, copied to shared memory a tile ahead of
+// their use (two buffers): rows of positions (x with the copy unit before it for the conv),
+// or channel-last rows of channels in scan order (x with 3 steps before it).
+template <typename T, int S, bool CL> struct BwdRaw {
+    using H = BwdShape<S>;
+    static constexpr int ES = (int)sizeof(T);
+    static constexpr int kXRow = CL ? H::G * ES : 16 + H::TT * ES;
+    static constexpr int kRow = CL ? H::G * ES : H::TT * ES;
+    static constexpr int kBRow = CL ? (H::NS * ES < 16 ? 16 : H::NS * ES) : H::TT * ES;
+    static constexpr int kRows = CL ? H::TT : H::G;
+    static constexpr int X = 0;
+    static constexpr int DT = X + (CL ? H::TT + 3 : H::G) * kXRow;
+    static constexpr int Z = DT + kRows * kRow;
+    static constexpr int DY = Z + kRows * kRow;
+    static constexpr int B = DY + kRows * kRow;
+    static constexpr int C = B + (CL ? H::TT : H::NS) * kBRow;
+    static constexpr int SC = C + (CL ? H::TT : H::NS) * kBRow;    // scales: 3 tensors x 2 blocks x G
+    static constexpr int SINCE = SC + 6 * H::G * 4;
+    static constexpr int BYTES = SINCE + 16;
 };
 
 // f[i] = element lo..hi-1 of a run (others 0) at p + i * step; one 16-byte (or two, or one
@@ -187,17 +223,39 @@ __device__ __forceinline__ int reduce8_first(int lane) {
     return off;
 }
 
-// Sum over the 32 / S channels of a warp of 32 values a lane (8 steps x 4 states):
-// afterwards a lane holds S sums, values reduce32_first(lane) and on.
+// Sum over the first NC channels of a lane's 4 values (one per state slot): each level
+// adds the partner's other half. Leaves 4 / NC values, of slots 0, 4 / NC, ...
 template <int S>
-__device__ __forceinline__ void reduce32(float (&v)[32], int lane) {
-    int cnt = 32;
+__device__ __forceinline__ void reduce_slots(const uint64_t (&v)[2], float* r) {
+    constexpr int NC = BwdShape<S>::NC;
+    const float2 a = upk2(v[0]), b = upk2(v[1]);
+    if constexpr (NC == 4) {
+        const float2 c = upk2(add2(v[0], pk2(__shfl_xor_sync(0xffffffffu, b.x, 2 * S),
+                                             __shfl_xor_sync(0xffffffffu, b.y, 2 * S))));
+        r[0] = c.x + __shfl_xor_sync(0xffffffffu, c.y, S);
+    } else if constexpr (NC == 2) {
+        r[0] = a.x + __shfl_xor_sync(0xffffffffu, a.y, S);
+        r[1] = b.x + __shfl_xor_sync(0xffffffffu, b.y, S);
+    } else {
+        r[0] = a.x;
+        r[1] = a.y;
+        r[2] = b.x;
+        r[3] = b.y;
+    }
+}
+
+// Sum over the remaining 32 / S / 4 groups of channels of 8 values (one per step): as
+// reduce8, over the upper lane bits. A lane keeps 8 / (8 / S) of them from
+// reduce_groups_first(lane).
+template <int S>
+__device__ __forceinline__ void reduce_groups(float (&v)[8], int lane) {
+    int cnt = 8;
 #pragma unroll
-    for (int w = S; w < 32; w *= 2) {
+    for (int w = 4 * S; w < 32; w *= 2) {
         cnt /= 2;
         const bool up = lane & w;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+        for (int k = 0; k < 4; ++k)
             if (k < cnt) {
                 const float send = up ? v[k] : v[k + cnt];
                 const float keep = up ? v[k + cnt] : v[k];
@@ -206,10 +264,10 @@ __device__ __forceinline__ void reduce32(float (&v)[32], int lane) {
     }
 }
 template <int S>
-__device__ __forceinline__ int reduce32_first(int lane) {
-    int off = 0, cnt = 32;
+__device__ __forceinline__ int reduce_groups_first(int lane) {
+    int off = 0, cnt = 8;
 #pragma unroll
-    for (int w = S; w < 32; w *= 2) {
+    for (int w = 4 * S; w < 32; w *= 2) {
         cnt /= 2;
         off += (lane & w) ? cnt : 0;
     }
@@ -252,62 +310,259 @@ __device__ __forceinline__ void load_prm(const BwdParams& p, int d0, float* prm)
     }
 }
 
-// Stage steps [t0, t0 + TT) (scan order) of the CTA's channels: {delta, delta u, g, start}
-// per channel and step, u where ADJ, and the rows of B (and C where ADJ). Steps past the
-// end and channels past dim stage zeros: a = 1 and no input, which leave both recurrences
-// where they are.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, int have) {
+    // BYTES (4, 8 or 16) to shared memory, the first `have` of them from src, zeros behind
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+                 "r"(have));
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Rows of positions: `rows` rows (channels or states, those below `have` exist) of the TT
+// positions from pos0 on. unit: bytes per copy, a multiple of the element size e.
+template <int TT, int UNIT>
+__device__ __forceinline__ void fetch_rows(const uint8_t* src, int64_t sc, int e, int L, int pos0,
+                                           int rows, int have, uint8_t* dst, int drow) {
+    const int per = TT * e / UNIT;
+    for (int i = threadIdx.x; i < rows * per; i += kBwdThreads) {
+        const int r = i / per, k = i % per, pos = pos0 + k * (UNIT / e);
+        const bool in = r < have && pos >= 0 && pos < L;
+        cp_async<UNIT>(dst + r * drow + k * UNIT, in ? src + ((int64_t)r * sc + pos) * e : src, in ? UNIT : 0);
+    }
+}
+template <int TT>
+__device__ __forceinline__ void fetch_rows_slow(const uint8_t* src, int64_t sc, int e, int L, int pos0,
+                                                int rows, int have, uint8_t* dst, int drow) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * TT; i += kBwdThreads) {
+        const int r = i / TT, k = i % TT, pos = pos0 + k;
+        const bool in = r < have && pos >= 0 && pos < L;
+        const uint8_t* q = src + ((int64_t)r * sc + pos) * e;
+        if (e == 4) reinterpret_cast<uint32_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+        else if (e == 2) reinterpret_cast<uint16_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
+        else (dst + r * drow)[k] = in ? *q : 0;
+    }
+}
+// Channel-last rows: `have` elements of the steps t0 .. t0 + rows - 1 (scan order).
+__device__ __forceinline__ void fetch_steps(const uint8_t* src, int64_t sp, int e, int L, int t0, bool rev,
+                                            int rows, int width, int have, uint8_t* dst, int drow, bool async) {
+    if (async) {
+        const int per = (width * e + 15) / 16;
+        for (int i = threadIdx.x; i < rows * per; i += kBwdThreads) {
+            const int r = i / per, k = i % per, t = t0 + r, pos = rev ? L - 1 - t : t;
+            const int n = t >= 0 && t < L ? min(16, max(0, have * e - 16 * k)) : 0;
+            cp_async<16>(dst + r * drow + k * 16, n ? src + (int64_t)pos * sp * e + k * 16 : src, n);
+        }
+        return;
+    }
+#pragma unroll 4
+    for (int i = threadIdx.x; i < rows * width; i += kBwdThreads) {
+        const int r = i / width, k = i % width, t = t0 + r, pos = rev ? L - 1 - t : t;
+        const bool in = t >= 0 && t < L && k < have;
+        const uint8_t* q = src + ((int64_t)pos * sp + k) * e;
+        if (e == 4) reinterpret_cast<uint32_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+        else if (e == 2) reinterpret_cast<uint16_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
+        else (dst + r * drow)[k] = in ? *q : 0;
+    }
+}
+
+// Start copying the inputs of steps [t0, t0 + TT) into a buffer: x, delta, B, and with ADJ z,
+// dout, C. Asynchronous copies where the host found every row aligned to the copy unit
+// (p.async), else plain loads.
 template <typename T, int S, bool CL, bool ADJ>
-__device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, int t0,
-                                           const float* prm, float4* st, float* us, float* Bs,
-                                           float* Cs) {
+__device__ __forceinline__ void fetch_tile(const BwdParams& p, int b, int d0, int t0, uint8_t* raw) {
     using H = BwdShape<S>;
+    using R = BwdRaw<T, S, CL>;
+    constexpr int TT = H::TT, ES = R::ES;
+    const int L = p.seqlen, pos0 = p.reverse ? L - t0 - TT : t0, have = p.dim - d0;
+    const int eq = p.x.scale ? 1 : ES;                         // bytes per element of x, delta, z
+    auto base = [&](const void* q, const Str& st, int e) {
+        return static_cast<const uint8_t*>(q) + ((int64_t)b * st.b + (int64_t)d0 * st.c) * e;
+    };
+    auto rows = [&](const uint8_t* src, int64_t sc, int e, int n, int hv, uint8_t* dst, int drow) {
+        if (!p.async) fetch_rows_slow<TT>(src, sc, e, L, pos0, n, hv, dst, drow);
+        else if (e == 1 && TT == 8) fetch_rows<TT, 8>(src, sc, e, L, pos0, n, hv, dst, drow);
+        else fetch_rows<TT, 16>(src, sc, e, L, pos0, n, hv, dst, drow);
+    };
+    auto act = [&](const void* q, const Str& st, int e, uint8_t* dst) {
+        if constexpr (CL) fetch_steps(base(q, st, e), st.p, e, L, t0, p.reverse, TT, H::G, have, dst, R::kRow, p.async);
+        else rows(base(q, st, e), st.c, e, H::G, have, dst, R::kRow);
+    };
+    auto bc = [&](const void* q, const Str& st, uint8_t* dst) {
+        const uint8_t* src = static_cast<const uint8_t*>(q) + (int64_t)b * st.b * ES;
+        if constexpr (CL) fetch_steps(src, st.p, ES, L, t0, p.reverse, TT, H::NS, p.dstate, dst, R::kBRow, p.async);
+        else rows(src, st.c, ES, H::NS, p.dstate, dst, R::kBRow);
+    };
+    const uint8_t* xb = base(p.x.p, p.x.s, eq);
+    if constexpr (CL) {
+        const int lead = p.conv_w ? 3 : 0;
+        fetch_steps(xb, p.x.s.p, eq, L, t0 - lead, p.reverse, TT + lead, H::G, have,
+                    raw + R::X + (3 - lead) * R::kXRow, R::kXRow, p.async);
+    } else {
+        rows(xb, p.x.s.c, eq, H::G, have, raw + R::X + 16, R::kXRow);
+        if (p.conv_w) {
+            // the 4 or more positions the conv reads before the tile (reverse: behind it)
+            if (p.async && eq * TT >= 16) {
+                const int he = 16 / eq;
+                for (int r = threadIdx.x; r < H::G; r += kBwdThreads) {
+                    const int pos = p.reverse ? pos0 + TT : pos0 - he;
+                    const bool in = r < have && pos >= 0 && pos < L;
+                    cp_async<16>(raw + R::X + r * R::kXRow, in ? xb + ((int64_t)r * p.x.s.c + pos) * eq : xb, in ? 16 : 0);
+                }
+            } else {
+                for (int i = threadIdx.x; i < H::G * 3; i += kBwdThreads) {
+                    // scan offsets -3 .. -1, in the places the copy above would put them
+                    const int r = i / 3, o = i % 3 - 3, t = t0 + o, pos = p.reverse ? L - 1 - t : t;
+                    const int at = p.reverse ? -1 - o : 16 / eq + o;
+                    const bool in = r < have && t >= 0 && t < L;
+                    const uint8_t* q = xb + ((int64_t)r * p.x.s.c + pos) * eq;
+                    uint8_t* dst = raw + R::X + r * R::kXRow;
+                    if (eq == 4) reinterpret_cast<uint32_t*>(dst)[at] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+                    else if (eq == 2) reinterpret_cast<uint16_t*>(dst)[at] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
+                    else dst[at] = in ? *q : 0;
+                }
+            }
+        }
+    }
+    act(p.dt.p, p.dt.s, eq, raw + R::DT);
+    bc(p.Bm, p.sB, raw + R::B);
+    if constexpr (ADJ) {
+        if (p.z.p) act(p.z.p, p.z.s, eq, raw + R::Z);
+        act(p.dy, p.sdy, ES, raw + R::DY);
+        bc(p.Cm, p.sC, raw + R::C);
+    }
+    if (p.x.scale) {
+        // a tile and its halo span at most two blocks of 64 positions: both their scales
+        const int last = (L - 1) / kBlock8;
+        const int lo = min(max(pos0 - 3, 0) / kBlock8, last), hi = min(max(pos0 + TT + 2, 0) / kBlock8, last);
+        for (int i = threadIdx.x; i < 6 * H::G; i += kBwdThreads) {
+            const int c = i % H::G, which = i / H::G, k = which / 2;
+            const ActIn& a = k == 0 ? p.x : k == 1 ? p.dt : p.z;
+            const bool in = c < have && a.scale && (k < 2 || ADJ);
+            const float* q = in ? a.scale + (int64_t)b * a.ss.b + (int64_t)(d0 + c) * a.ss.c +
+                                      (int64_t)(which % 2 ? hi : lo) * a.ss.p
+                                : p.x.scale;
+            cp_async<4>(raw + R::SC + 4 * i, q, in ? 4 : 0);
+        }
+    }
+    if (p.since && threadIdx.x == 0) cp_async<TT>(raw + R::SINCE, p.since + t0, TT);
+    cp_async_commit();
+}
+
+// N elements at p (dense, aligned to their size together), reversed if rev.
+template <typename T, int N>
+__device__ __forceinline__ void take_run(const T* p, bool rev, float (&f)[N]) {
+    constexpr int BY = N * (int)sizeof(T);
+    constexpr int V = BY >= 16 ? 16 : BY;
+    alignas(16) T e[N];
+#pragma unroll
+    for (int k = 0; k < BY / V; ++k) {
+        if constexpr (V == 16) reinterpret_cast<uint4*>(e)[k] = reinterpret_cast<const uint4*>(p)[k];
+        else if constexpr (V == 8) reinterpret_cast<uint2*>(e)[k] = reinterpret_cast<const uint2*>(p)[k];
+        else if constexpr (V == 4) reinterpret_cast<uint32_t*>(e)[k] = reinterpret_cast<const uint32_t*>(p)[k];
+        else reinterpret_cast<uint16_t*>(e)[k] = reinterpret_cast<const uint16_t*>(p)[k];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const T v = rev ? e[N - 1 - i] : e[i];
+        if constexpr (sizeof(T) == 1) f[i] = (float)v;
+        else f[i] = Elem<T>::to_f(v);
+    }
+}
+
+// A thread's run of EPT values of x, delta or z (which = 0, 1, 2; codes where packed) or of
+// dout (which = 3), in scan order; for x shift steps earlier (channel-last only).
+template <typename T, int S, bool CL>
+__device__ __forceinline__ void take(const BwdParams& p, const uint8_t* raw, int which,
+                                     const BwdRun<S, CL>& r, int t0, float (&f)[BwdShape<S>::EPT],
+                                     int shift = 0) {
+    using H = BwdShape<S>;
+    using R = BwdRaw<T, S, CL>;
     constexpr int E = H::EPT;
-    const int tid = threadIdx.x, L = p.seqlen, dir = p.reverse ? -1 : 1;
+    const bool q8 = p.x.scale && which < 3, rev = !CL && p.reverse;
+    const uint8_t* row = raw + (which == 0 ? R::X + (CL ? (r.tl + 3 - shift) * R::kXRow : r.ch * R::kXRow + 16)
+                                : (which == 1 ? R::DT : which == 2 ? R::Z : R::DY) + (CL ? r.tl : r.ch) * R::kRow);
+    const int at = CL ? r.ch : rev ? H::TT - E - r.tl : r.tl;
+    if (!q8) {
+        take_run<T, E>(reinterpret_cast<const T*>(row) + at, rev, f);
+        return;
+    }
+    take_run<int8_t, E>(reinterpret_cast<const int8_t*>(row) + at, rev, f);
+    const float* sc = reinterpret_cast<const float*>(raw + R::SC) + which * 2 * H::G;
+    const int pos0 = p.reverse ? p.seqlen - t0 - H::TT : t0;
+    const int lo = max(pos0 - 3, 0) / kBlock8;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int t = t0 + r.t(i) - shift, pos = p.reverse ? p.seqlen - 1 - t : t;
+        f[i] *= sc[(pos / kBlock8 == lo ? 0 : H::G) + r.c(i)];
+    }
+}
+
+// Turn a tile's raw inputs into what the recurrences take: delta and delta u (each twice, as
+// the pairs they take) per channel and step, g and u where ADJ, and the rows of B (and C
+// where ADJ) in each order of the states. Steps past the end and channels past dim get
+// zeros: a = 1 and no input, which leave both recurrences where they are.
+template <typename T, int S, bool CL, bool ADJ>
+__device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, int t0, const uint8_t* raw,
+                                           const float* prm, float4* st, float2* gs, float* us,
+                                           float* Bs, float* Cs, uint32_t* mask) {
+    using H = BwdShape<S>;
+    using R = BwdRaw<T, S, CL>;
+    constexpr int E = H::EPT;
+    const int tid = threadIdx.x, L = p.seqlen;
     const BwdRun<S, CL> r(tid);
     const int d = d0 + r.ch, t = t0 + r.tl;
-    const int pos = p.reverse ? L - 1 - t : t;
     // valid elements of the run: [0, hi)
     const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
+    const uint8_t* since = raw + R::SINCE;
     float u[E], dt[E], g[E];
+    take<T, S, CL>(p, raw, 0, r, t0, u);
     if (p.conv_w) {
         float acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = prm[r.c(i) * 8 + 4];
+        // x at scan position tm < 0 of channel c: the history
+        auto past = [&](int c, int tm) {
+            return p.hist && d0 + c < p.dim && tm >= -(p.conv_width - 1)
+                       ? Elem<T>::to_f(static_cast<const T*>(
+                             p.hist)[((int64_t)b * p.dim + d0 + c) * (p.conv_width - 1) + (p.conv_width - 1 + tm)])
+                       : 0.f;
+        };
         if constexpr (CL) {
-            const int sn = p.since && t < L ? p.since[t] : 4;
-            for (int lag = 0; lag < p.conv_width; ++lag) {
-                if (lag > sn) break;
+            const int sn = p.since ? since[r.tl] : 4;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = fmaf(prm[r.c(i) * 8 + 3], u[i], acc[i]);
+#pragma unroll
+            for (int lag = 1; lag < 4; ++lag) {
                 float x[E];
-                if (t - lag >= 0) {
-                    load_act<T, E>(p.x, b, d, pos - dir * lag, dir, false, 0, hi, x);
-                } else {
+                take<T, S, CL>(p, raw, 0, r, t0, x, lag);
+                if (t - lag < 0)
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const T* h = static_cast<const T*>(p.hist);
-                        x[i] = h && i < hi ? Elem<T>::to_f(h[((int64_t)b * p.dim + d + i) * (p.conv_width - 1) +
-                                                            (p.conv_width - 1 + t - lag)])
-                                           : 0.f;
-                    }
-                }
+                    for (int i = 0; i < E; ++i) x[i] = past(r.ch + i, t - lag);
+                if (lag <= sn)
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(prm[r.c(i) * 8 + 3 - lag], x[i], acc[i]);
+                    for (int i = 0; i < E; ++i) acc[i] = fmaf(prm[r.c(i) * 8 + 3 - lag], x[i], acc[i]);
             }
         } else {
-            float x[E], xh[3];                                 // the run, and the 3 steps before
-            load_act<T, E>(p.x, b, d, pos, dir, true, 0, hi, x);
+            float xh[3];                                       // the 3 steps before the run
+            const uint8_t* row = raw + R::X + r.ch * R::kXRow;
+            const int eq = p.x.scale ? 1 : R::ES;
+            const float* sc = reinterpret_cast<const float*>(raw + R::SC);
+            const int pos0 = p.reverse ? L - t0 - H::TT : t0, blk0 = max(pos0 - 3, 0) / kBlock8;
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
-                const int tm = t - 3 + m;
-                xh[m] = 0.f;
-                if (hi > 0 && 3 - m < p.conv_width) {
-                    if (tm >= 0) {
-                        float one[1];
-                        load_act<T, 1>(p.x, b, d, pos - dir * (3 - m), dir, true, 0, 1, one);
-                        xh[m] = one[0];
-                    } else if (p.hist && tm >= -(p.conv_width - 1)) {
-                        xh[m] = Elem<T>::to_f(static_cast<const T*>(
-                            p.hist)[((int64_t)b * p.dim + d) * (p.conv_width - 1) + (p.conv_width - 1 + tm)]);
-                    }
+                const int o = r.tl - 3 + m;                    // scan offset within the tile
+                const int at = o >= 0 ? 16 / eq + (p.reverse ? H::TT - 1 - o : o)
+                                      : p.reverse ? -1 - o : 16 / eq + o;
+                if (t0 + o < 0) {
+                    xh[m] = past(r.ch, t0 + o);
+                } else if (p.x.scale) {
+                    const int pos = p.reverse ? L - 1 - (t0 + o) : t0 + o;
+                    xh[m] = (float)reinterpret_cast<const int8_t*>(row)[at] *
+                            sc[(pos / kBlock8 == blk0 ? 0 : H::G) + r.ch];
+                } else {
+                    xh[m] = Elem<T>::to_f(reinterpret_cast<const T*>(row)[at]);
                 }
             }
             float w[4];
@@ -315,51 +570,61 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
             for (int k = 0; k < 4; ++k) w[k] = prm[r.ch * 8 + k];
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const int sn = p.since && i < hi ? p.since[t + i] : 4;
+                const int sn = p.since ? since[r.tl + i] : 4;
 #pragma unroll
                 for (int lag = 0; lag < 4; ++lag) {
-                    const float v = i >= lag ? x[i >= lag ? i - lag : 0] : xh[i >= lag ? 0 : 3 + i - lag];
+                    const float v = i >= lag ? u[i >= lag ? i - lag : 0] : xh[i >= lag ? 0 : 3 + i - lag];
                     if (lag <= sn) acc[i] = fmaf(w[3 - lag], v, acc[i]);
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) u[i] = i < hi ? silu(acc[i]) : 0.f;
-    } else {
-        load_act<T, E>(p.x, b, d, pos, dir, !CL, 0, hi, u);
+        for (int i = 0; i < E; ++i) u[i] = silu(acc[i]);
     }
-    load_act<T, E>(p.dt, b, d, pos, dir, !CL, 0, hi, dt);
+    take<T, S, CL>(p, raw, 1, r, t0, dt);
     if constexpr (ADJ) {
-        const T* dy = static_cast<const T*>(p.dy) + (int64_t)b * p.sdy.b + (int64_t)d * p.sdy.c +
-                      (int64_t)pos * p.sdy.p;
-        load_run<T, E>(dy, CL ? p.sdy.c : dir * p.sdy.p, 0, hi, g);
+        take<T, S, CL>(p, raw, 3, r, t0, g);
         if (p.z.p) {
             float z[E];
-            load_act<T, E>(p.z, b, d, pos, dir, !CL, 0, hi, z);
+            take<T, S, CL>(p, raw, 2, r, t0, z);
 #pragma unroll
             for (int i = 0; i < E; ++i) g[i] *= silu(z[i]);
         }
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        const float raw = dt[i] + prm[r.c(i) * 8 + 5];
-        float dl = p.softplus ? (raw > 20.f ? raw : softplus(raw)) : raw;
-        if (i >= hi) dl = 0.f;
-        const float start = p.since && i < hi && p.since[t0 + r.t(i)] == 0 ? -INFINITY : 0.f;
-        st[r.c(i) * (H::TT + 1) + r.t(i)] = make_float4(dl, dl * u[i], ADJ ? g[i] : 0.f, start);
-        if constexpr (ADJ) us[r.c(i) * (H::TT + 1) + r.t(i)] = u[i];
+        const float raw_dt = dt[i] + prm[r.c(i) * 8 + 5];
+        float dl = p.softplus ? (raw_dt > 20.f ? raw_dt : softplus(raw_dt)) : raw_dt;
+        if (i >= hi) {
+            dl = u[i] = 0.f;
+            if (ADJ) g[i] = 0.f;
+        }
+        const int o = r.c(i) * (H::TT + 1) + r.t(i);
+        const float du = dl * u[i];
+        st[o] = make_float4(dl, dl, du, du);
+        if constexpr (ADJ) {
+            gs[o] = make_float2(g[i], g[i]);
+            us[o] = u[i];
+        }
+    }
+    if (tid < 32) {
+        const uint32_t m = __ballot_sync(0xffffffffu, p.since && tid < H::TT && t0 + tid < L &&
+                                                          since[tid < H::TT ? tid : 0] == 0);
+        if (tid == 0) *mask = m;
     }
     // rows of B and C
-    const T* Bp = static_cast<const T*>(p.Bm) + (int64_t)b * p.sB.b;
-    const T* Cp = static_cast<const T*>(p.Cm) + (int64_t)b * p.sC.b;
+    const T* Br = reinterpret_cast<const T*>(raw + R::B);
+    const T* Cr = reinterpret_cast<const T*>(raw + R::C);
 #pragma unroll 4
     for (int k = tid; k < H::NS * H::TT; k += kBwdThreads) {
-        const int n = CL ? k % H::NS : k / H::TT, tl = CL ? k / H::NS : k % H::TT;
-        const int tt = t0 + tl, ps = p.reverse ? L - 1 - tt : tt;
-        const bool in = n < p.dstate && tt < L;
-        Bs[tl * H::RB + n] = in ? Elem<T>::to_f(Bp[(int64_t)n * p.sB.c + (int64_t)ps * p.sB.p]) : 0.f;
-        if constexpr (ADJ)
-            Cs[tl * H::RB + n] = in ? Elem<T>::to_f(Cp[(int64_t)n * p.sC.c + (int64_t)ps * p.sC.p]) : 0.f;
+        const int n = k % H::NS, tl = k / H::NS;
+        const int at = CL ? tl * (R::kBRow / R::ES) + n : n * H::TT + (p.reverse ? H::TT - 1 - tl : tl);
+        const float bv = Elem<T>::to_f(Br[at]), cv = ADJ ? Elem<T>::to_f(Cr[at]) : 0.f;
+#pragma unroll
+        for (int q = 0; q < H::NC; ++q) {
+            Bs[(q * H::TT + tl) * H::RB + (n ^ q)] = bv;
+            if constexpr (ADJ) Cs[(q * H::TT + tl) * H::RB + (n ^ q)] = cv;
+        }
     }
 }
 
@@ -369,7 +634,7 @@ __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int n = 4 * j + k;
+        const int n = 4 * j + (k ^ slot_order<S>(d));
         const bool in = d < p.dim && n < p.dstate;
         a[k] = !in ? 0.f : kLog2e * (HEADS ? p.A[d / p.head_dim] : p.A[(int64_t)d * p.dstate + n]);
     }
@@ -377,20 +642,36 @@ __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_
     A2[1] = pk2(a[2], a[3]);
 }
 
-// Decay of one step for a lane's 4 states: 2^(delta A log2 e + start), start = -inf at a
-// sequence's first step. With A per head one exp serves all.
+// Decay of one step for a lane's 4 states: 2^(delta A log2 e). With A per head one exp
+// serves all. d2: delta twice.
 template <bool HEADS>
-__device__ __forceinline__ void decay(const uint64_t (&A2)[2], float dl, float start, uint64_t (&a)[2]) {
+__device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint64_t (&a)[2]) {
     if constexpr (HEADS) {
-        const float e = ex2(fmaf(dl, lo2(A2[0]), start));
+        const float e = ex2(lo2(d2) * lo2(A2[0]));
         a[0] = a[1] = pk2(e, e);
     } else {
-        const uint64_t d2 = pk2(dl, dl), o2 = pk2(start, start);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const float2 x = upk2(fma2(d2, A2[k], o2));
+            const float2 x = upk2(mul2(d2, A2[k]));
             a[k] = pk2(ex2(x.x), ex2(x.y));
         }
+    }
+}
+
+// Decays of the kSubSteps steps from row, zero at the sequence starts in mask.
+template <bool HEADS>
+__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float4* row, uint32_t mask,
+                                       uint64_t (&a)[kSubSteps][2], uint64_t (&du2)[kSubSteps]) {
+#pragma unroll
+    for (int i = 0; i < kSubSteps; ++i) {
+        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(row + i);
+        decay<HEADS>(A2, s.x, a[i]);
+        du2[i] = s.y;
+    }
+    if (mask) {
+#pragma unroll
+        for (int i = 0; i < kSubSteps; ++i)
+            if (mask >> i & 1) a[i][0] = a[i][1] = 0;
     }
 }
 
@@ -403,13 +684,14 @@ __device__ __forceinline__ void stpair(float* s, const uint64_t (&v)[2]) {
     *reinterpret_cast<ulonglong2*>(s) = make_ulonglong2(v[0], v[1]);
 }
 
-// Four states of a (batch, dim, dstate) tensor, zeros past dim or d_state or when null.
+// A lane's states of a (batch, dim, dstate) tensor, zeros past dim or d_state or when null.
+template <int S>
 __device__ __forceinline__ void load_state(const BwdParams& p, const float* s, int b, int d, int j,
                                            uint64_t (&v)[2]) {
     float f[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int n = 4 * j + k;
+        const int n = 4 * j + (k ^ slot_order<S>(d));
         f[k] = s && d < p.dim && n < p.dstate ? s[((int64_t)b * p.dim + d) * p.dstate + n] : 0.f;
     }
     v[0] = pk2(f[0], f[1]);
@@ -429,10 +711,14 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
     constexpr bool SUM = MODE == kSummary;
     extern __shared__ __align__(16) float sm[];
     float4* st = reinterpret_cast<float4*>(sm);
-    float* us = sm + H::kSt;
+    float2* gs = reinterpret_cast<float2*>(sm + H::kSt);
+    float* us = sm + H::kSt + (SUM ? H::kG : 0);
     float* Bs = us + (SUM ? H::kU : 0);
     float* Cs = Bs + H::kBC;
     float* prm = Cs + (SUM ? H::kBC : 0);
+    uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
+    uint8_t* raw = reinterpret_cast<uint8_t*>(prm + H::kPrm + H::kMask);
+    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int j = lane % S, cl = lane / S;
     const int b = blockIdx.y, d0 = blockIdx.x * H::G, seg = blockIdx.z;
@@ -447,35 +733,43 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
         R[kc][0] = R[kc][1] = 0;
         P[kc][0] = P[kc][1] = pk2(1.f, 1.f);
         h[kc][0] = h[kc][1] = 0;
-        if (!SUM && seg == 0) load_state(p, p.h0, b, d, j, h[kc]);
+        if (!SUM && seg == 0) load_state<S>(p, p.h0, b, d, j, h[kc]);
         if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc]);
     }
-    for (int t0 = tb; t0 < te; t0 += H::TT) {
+    fetch_tile<T, S, CL, SUM>(p, b, d0, tb, raw);
+    int buf = 0;
+    for (int t0 = tb; t0 < te; t0 += H::TT, buf ^= 1) {
+        cp_async_wait();
+        __syncthreads();                                       // this tile is here, the last one used
+        if (t0 + H::TT < te) fetch_tile<T, S, CL, SUM>(p, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
+        stage_tile<T, S, CL, SUM>(p, b, d0, t0, raw + buf * kRaw, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
-        stage_tile<T, S, CL, SUM>(p, b, d0, t0, prm, st, us, Bs, Cs);
-        __syncthreads();
+        const uint32_t starts = *mask;
 #pragma unroll
         for (int kc = 0; kc < H::KC; ++kc) {
-            const int c = (warp * H::KC + kc) * H::CW + cl, d = d0 + c;
-            const float4* srow = st + c * (H::TT + 1);
+            const int c = (warp * H::KC + kc) * H::CW + cl, d = d0 + c, q = slot_order<S>(d);
 #pragma unroll 1
             for (int sub = 0; sub < H::NSUB; ++sub) {
                 if (!SUM && d < p.dim)
                     stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / kSubSteps + sub, d, j), h[kc]);
+                const int o = c * (H::TT + 1) + sub * kSubSteps;
+                const float* Br = Bs + (q * H::TT + sub * kSubSteps) * H::RB + 4 * j;
+                const float* Cr = Cs + (q * H::TT + sub * kSubSteps) * H::RB + 4 * j;
+                uint64_t a[kSubSteps][2], du2[kSubSteps];
+                decays<HEADS>(A2[kc], st + o, starts >> (sub * kSubSteps) & 255, a, du2);
 #pragma unroll
                 for (int i = 0; i < kSubSteps; ++i) {
-                    const int tl = sub * kSubSteps + i;
-                    const float4 s = srow[tl];
-                    uint64_t a[2], bv[2], cv[2];
-                    decay<HEADS>(A2[kc], s.x, s.w, a);
-                    ldpair(Bs + tl * H::RB + 4 * j, bv);
-                    if (SUM) ldpair(Cs + tl * H::RB + 4 * j, cv);
-                    const uint64_t du2 = pk2(s.y, s.y), g2 = pk2(s.z, s.z);
+                    uint64_t bv[2], cv[2], g2 = 0;
+                    ldpair(Br + i * H::RB, bv);
+                    if (SUM) {
+                        ldpair(Cr + i * H::RB, cv);
+                        g2 = *reinterpret_cast<const uint64_t*>(gs + o + i);
+                    }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        h[kc][k] = fma2(a[k], h[kc][k], mul2(du2, bv[k]));
+                        h[kc][k] = fma2(a[i][k], h[kc][k], mul2(du2[i], bv[k]));
                         if (SUM) {
-                            P[kc][k] = mul2(P[kc][k], a[k]);
+                            P[kc][k] = mul2(P[kc][k], a[i][k]);
                             R[kc][k] = fma2(P[kc][k], mul2(g2, cv[k]), R[kc][k]);
                         }
                     }
@@ -499,13 +793,14 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
 
 // Chains the segments' summaries: sumS[seg] becomes the state before the segment, sumR[seg]
 // the adjoint carry a_t lam_t from behind it. One thread per (batch row, channel, state).
-template <int NS>
+template <int S>
 __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) {
+    constexpr int NS = 4 * S;
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t per = (int64_t)p.batch * p.dim * NS;
     if (idx >= per) return;
-    const int n = (int)(idx % NS);
     const int64_t bd = idx / NS;
+    const int n = (int)(idx % NS) ^ slot_order<S>((int)(bd % p.dim));
     float h = p.h0 && n < p.dstate ? p.h0[bd * p.dstate + n] : 0.f;
     float m = p.dhl && n < p.dstate ? p.dhl[bd * p.dstate + n] : 0.f;
     for (int s = 0; s < p.nseg; ++s) {
@@ -524,13 +819,14 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
 
 // The backward sweep.
 template <typename T, int S, bool CL, bool HEADS>
-__global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr int KC = H::KC, TT = H::TT, E = H::EPT;
     constexpr bool REGS = KC <= 2;                             // m and dA of every slot in registers
     extern __shared__ __align__(16) float sm[];
     float4* st = reinterpret_cast<float4*>(sm);
-    float* us = sm + H::kSt;
+    float2* gs = reinterpret_cast<float2*>(sm + H::kSt);
+    float* us = sm + H::kSt + H::kG;
     float* ys = us + H::kU;
     float* s1s = ys + H::kOut;
     float* s2s = s1s + H::kOut;
@@ -538,8 +834,11 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
     float* Cs = Bs + H::kBC;
     float* part = Cs + H::kBC;
     float* prm = part + H::kPart;
-    float* carry = prm + H::kPrm;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
+    float* carry = prm + H::kPrm + H::kMask;
     float* sums = carry + H::kCarry;
+    uint8_t* raw = reinterpret_cast<uint8_t*>(sums + (CL ? H::kSum : 0));
+    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int j = lane % S, cl = lane / S;
     const int b = blockIdx.y, d0 = blockIdx.x * H::G, seg = blockIdx.z;
@@ -554,7 +853,7 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
         const int r = REGS ? kc : 0;
         dA[r][0] = dA[r][1] = 0;
         m[r][0] = m[r][1] = 0;
-        if (te == L) load_state(p, p.dhl, b, d, j, m[r]);
+        if (te == L) load_state<S>(p, p.dhl, b, d, j, m[r]);
         else if (d < p.dim) ldpair(p.sumR + ns_off<S>(p, row, d, j), m[r]);
         if constexpr (REGS) {
             load_A<S, HEADS>(p, d, j, A2[r]);
@@ -570,73 +869,87 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
     }
 
     const int ntiles = (te - tb + TT - 1) / TT;
-    for (int tile = ntiles - 1; tile >= 0; --tile) {
+    // the states before sub-tile `sub` of a tile, for slot kc; fetched one use ahead
+    auto load_ckpt = [&](int tile, int sub, int kc, uint64_t (&v)[2]) {
+        const int d = d0 + (warp * KC + kc) * H::CW + cl;
+        if (d < p.dim)
+            ldpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + (tb + tile * TT) / kSubSteps + sub, d, j), v);
+    };
+    uint64_t hn[2] = {0, 0};
+    load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
+    fetch_tile<T, S, CL, true>(p, b, d0, tb + (ntiles - 1) * TT, raw);
+    int buf = 0;
+    for (int tile = ntiles - 1; tile >= 0; --tile, buf ^= 1) {
         const int t0 = tb + tile * TT;
+        const uint8_t* cur = raw + buf * kRaw;
+        cp_async_wait();
+        __syncthreads();                                       // this tile is here, the last one used
+        if (tile > 0) fetch_tile<T, S, CL, true>(p, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
+        stage_tile<T, S, CL, true>(p, b, d0, t0, cur, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
-        stage_tile<T, S, CL, true>(p, b, d0, t0, prm, st, us, Bs, Cs);
-        __syncthreads();
+        const uint32_t starts = *mask;
 #pragma unroll 1
         for (int sub = H::NSUB - 1; sub >= 0; --sub) {
-            float vB[32], vC[32];
+            constexpr int PT = 4 / H::NC;                      // values left per step
+            float rB[8 * PT], rC[8 * PT];
             if constexpr (KC > 1) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) vB[i] = vC[i] = 0.f;
+                for (int i = 0; i < 8 * PT; ++i) rB[i] = rC[i] = 0.f;
             }
             constexpr int UNR = REGS ? KC : 1;
 #pragma unroll UNR
             for (int kc = 0; kc < KC; ++kc) {
-                const int c = (warp * KC + kc) * H::CW + cl, d = d0 + c;
+                const int c = (warp * KC + kc) * H::CW + cl, d = d0 + c, sq = slot_order<S>(d);
                 const int r = REGS ? kc : 0;
-                uint64_t h0[2] = {0, 0};
-                if (d < p.dim)
-                    ldpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / kSubSteps + sub, d, j), h0);
+                const uint64_t h0[2] = {hn[0], hn[1]};
+                if (kc + 1 < KC) load_ckpt(tile, sub, kc + 1, hn);
+                else if (sub > 0) load_ckpt(tile, sub - 1, 0, hn);
+                else if (tile > 0) load_ckpt(tile - 1, H::NSUB - 1, 0, hn);
                 if constexpr (!REGS) {
                     load_A<S, HEADS>(p, d, j, A2[0]);
                     ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
                     ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
                 }
-                const float4* srow = st + c * (TT + 1) + sub * kSubSteps;
-                const float* Br = Bs + sub * kSubSteps * H::RB + 4 * j;
-                const float* Cr = Cs + sub * kSubSteps * H::RB + 4 * j;
+                const int so = c * (TT + 1) + sub * kSubSteps;
+                const float* Br = Bs + (sq * TT + sub * kSubSteps) * H::RB + 4 * j;
+                const float* Cr = Cs + (sq * TT + sub * kSubSteps) * H::RB + 4 * j;
                 uint64_t a[kSubSteps][2], h[kSubSteps][2];
+                {
+                    uint64_t du2[kSubSteps];
+                    decays<HEADS>(A2[r], st + so, starts >> (sub * kSubSteps) & 255, a, du2);
 #pragma unroll
-                for (int i = 0; i < kSubSteps; ++i) {
-                    const float4 s = srow[i];
-                    uint64_t bv[2];
-                    decay<HEADS>(A2[r], s.x, s.w, a[i]);
-                    ldpair(Br + i * H::RB, bv);
-                    const uint64_t du2 = pk2(s.y, s.y);
+                    for (int i = 0; i < kSubSteps; ++i) {
+                        uint64_t bv[2];
+                        ldpair(Br + i * H::RB, bv);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        h[i][k] = fma2(a[i][k], i ? h[i ? i - 1 : 0][k] : h0[k], mul2(du2, bv[k]));
+                        for (int k = 0; k < 2; ++k)
+                            h[i][k] = fma2(a[i][k], i ? h[i ? i - 1 : 0][k] : h0[k], mul2(du2[i], bv[k]));
+                    }
                 }
                 float y[8], s1[8], s2[8];
 #pragma unroll
                 for (int i = kSubSteps - 1; i >= 0; --i) {
-                    const float4 s = srow[i];
-                    uint64_t bv[2], cv[2], lam[2], q[2];
+                    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(st + so + i);
+                    const uint64_t g2 = *reinterpret_cast<const uint64_t*>(gs + so + i);
+                    uint64_t bv[2], cv[2], lam[2], q[2], tb2[2], tc2[2];
                     ldpair(Br + i * H::RB, bv);
                     ldpair(Cr + i * H::RB, cv);
-                    const uint64_t d2 = pk2(s.x, s.x), du2 = pk2(s.y, s.y), g2 = pk2(s.z, s.z);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         lam[k] = fma2(g2, cv[k], m[r][k]);
                         m[r][k] = mul2(a[i][k], lam[k]);
                         q[k] = mul2(m[r][k], i ? h[i ? i - 1 : 0][k] : h0[k]);
-                        dA[r][k] = fma2(q[k], d2, dA[r][k]);
-                        const int v = 4 * i + 2 * k;
-                        float2 fb, fc;                         // summed over the warp's slots
-                        if constexpr (KC > 1) {
-                            fb = upk2(fma2(lam[k], du2, pk2(vB[v], vB[v + 1])));
-                            fc = upk2(fma2(g2, h[i][k], pk2(vC[v], vC[v + 1])));
-                        } else {
-                            fb = upk2(mul2(lam[k], du2));
-                            fc = upk2(mul2(g2, h[i][k]));
-                        }
-                        vB[v] = fb.x;
-                        vB[v + 1] = fb.y;
-                        vC[v] = fc.x;
-                        vC[v + 1] = fc.y;
+                        dA[r][k] = fma2(q[k], s.x, dA[r][k]);
+                        tb2[k] = mul2(lam[k], s.y);
+                        tc2[k] = mul2(g2, h[i][k]);
+                    }
+                    float vb[PT], vc[PT];
+                    reduce_slots<S>(tb2, vb);
+                    reduce_slots<S>(tc2, vc);
+#pragma unroll
+                    for (int k = 0; k < PT; ++k) {
+                        rB[i * PT + k] = KC > 1 ? rB[i * PT + k] + vb[k] : vb[k];
+                        rC[i * PT + k] = KC > 1 ? rC[i * PT + k] + vc[k] : vc[k];
                     }
                     const float2 fy = upk2(fma2(cv[1], h[i][1], mul2(cv[0], h[i][0])));
                     const float2 f1 = upk2(fma2(bv[1], lam[1], mul2(bv[0], lam[0])));
@@ -668,15 +981,26 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
                     stpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
                 }
             }
-            reduce32<S>(vB, lane);
-            reduce32<S>(vC, lane);
-            const int first = reduce32_first<S>(lane);
+            const int sq = slot_order<S>(cl);
+            if constexpr (PT == 1) {
+                reduce_groups<S>(rB, lane);
+                reduce_groups<S>(rC, lane);
+                const int first = reduce_groups_first<S>(lane);
+                constexpr int CNT = S >= 8 ? 8 : S;            // 8 steps over 8 / S groups
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
-                const int v = first + k, tl = sub * kSubSteps + v / 4, n = 4 * j + v % 4;
-                float* o = part + ((warp * TT + tl) * 2) * H::NS + n;
-                o[0] = vB[k];
-                o[H::NS] = vC[k];
+                for (int k = 0; k < CNT; ++k) {
+                    float* o = part + ((warp * TT + sub * kSubSteps + first + k) * 2) * H::NS + 4 * j + sq;
+                    o[0] = rB[k];
+                    o[H::NS] = rC[k];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8 * PT; ++k) {             // slot k % PT * NC of step k / PT
+                    float* o = part + ((warp * TT + sub * kSubSteps + k / PT) * 2) * H::NS + 4 * j +
+                               (k % PT * H::NC ^ sq);
+                    o[0] = rB[k];
+                    o[H::NS] = rC[k];
+                }
             }
         }
         __syncthreads();
@@ -687,20 +1011,19 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
             const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
             if (hi > 0) {
                 float dt[E], z[E], dy[E], du[E], ddt[E], dz[E];
-                load_act<T, E>(p.dt, b, d, pos, dir, !CL, 0, hi, dt);
+                take<T, S, CL>(p, cur, 1, run, t0, dt);
                 if (p.z.p) {
-                    load_act<T, E>(p.z, b, d, pos, dir, !CL, 0, hi, z);
-                    load_run<T, E>(static_cast<const T*>(p.dy) + (int64_t)b * p.sdy.b +
-                                       (int64_t)d * p.sdy.c + (int64_t)pos * p.sdy.p,
-                                   CL ? p.sdy.c : dir * p.sdy.p, 0, hi, dy);
+                    take<T, S, CL>(p, cur, 2, run, t0, z);
+                    take<T, S, CL>(p, cur, 3, run, t0, dy);
                 }
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const int c = run.c(i), tl = run.t(i), o = c * (TT + 2) + tl;
                     const float4 s = st[c * (TT + 1) + tl];
+                    const float g = gs[c * (TT + 1) + tl].x;
                     const float u = us[c * (TT + 1) + tl], Dv = prm[c * 8 + 6];
                     const float s1 = s1s[o], s2 = s2s[o] * kLn2;
-                    du[i] = fmaf(s.z, Dv, s.x * s1);
+                    du[i] = fmaf(g, Dv, s.x * s1);
                     const float ddelta = fmaf(u, s1, s2);
                     ddt[i] = p.softplus ? ddelta * sigmoidf_(dt[i] + prm[c * 8 + 5]) : ddelta;
                     if (p.z.p) {
@@ -709,11 +1032,11 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
                     }
                     if (CL) {
                         if (i < hi) {
-                            sums[c * TT + tl] += s.z * u;
+                            sums[c * TT + tl] += g * u;
                             sums[H::G * TT + c * TT + tl] += ddt[i];
                         }
                     } else if (i < hi) {
-                        dD = fmaf(s.z, u, dD);
+                        dD = fmaf(g, u, dD);
                         dBias += ddt[i];
                     }
                 }
@@ -756,8 +1079,10 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_kernel(const BwdParams p
                 const float2 lo = upk2(m[r][0]), hi = upk2(m[r][1]);
                 const float f[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (4 * j + k < p.dstate) p.dh0[((int64_t)b * p.dim + d) * p.dstate + 4 * j + k] = f[k];
+                for (int k = 0; k < 4; ++k) {
+                    const int n = 4 * j + (k ^ slot_order<S>(d));
+                    if (n < p.dstate) p.dh0[((int64_t)b * p.dim + d) * p.dstate + n] = f[k];
+                }
             }
         }
     }

@@ -20,16 +20,17 @@ inline cudaError_t launch_with_smem(K k, dim3 grid, int smem, const BwdParams& p
 template <typename T, int S, bool CL, bool HEADS>
 inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t st) {
     using H = BwdShape<S>;
+    constexpr int kRaw = 2 * BwdRaw<T, S, CL>::BYTES;
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, HEADS, kCheckpoint>, grid,
-                                (H::kSt + H::kBC + H::kPrm) * 4, p, st);
+                                (H::kSt + H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
     if (what == 1)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, HEADS, kSummary>, grid,
-                                (H::kSt + H::kU + 2 * H::kBC + H::kPrm) * 4, p, st);
+                                (H::kSt + H::kG + H::kU + 2 * H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
     return launch_with_smem(scan_bwd_kernel<T, S, CL, HEADS>, grid,
-                            (H::kSt + H::kU + 3 * H::kOut + 2 * H::kBC + H::kPart + H::kPrm +
-                             H::kCarry + (CL ? H::kSum : 0)) * 4,
+                            (H::kSt + H::kG + H::kU + 3 * H::kOut + 2 * H::kBC + H::kPart + H::kPrm +
+                             H::kMask + H::kCarry + (CL ? H::kSum : 0)) * 4 + kRaw,
                             p, st);
 }
 

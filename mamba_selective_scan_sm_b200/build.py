@@ -12,6 +12,8 @@ LIB = os.path.join(PKG, "libssm_b200.so")
 SOURCES = ["kernels.cu", "scan_bf16.cu", "scan_f32.cu", "scan_bf16_ext.cu", "scan_f32_ext.cu",
            "scan_bf16_m2.cu", "scan_f32_m2.cu", "ssm_api.cu", "noalloc.cu",
            "scan_bwd_bf16.cu", "scan_bwd_bf16_cl.cu", "scan_bwd_f32.cu", "scan_bwd_f32_cl.cu",
+           "scan_bwd_bf16_q8.cu", "scan_bwd_bf16_cl_q8.cu", "scan_bwd_f32_q8.cu",
+           "scan_bwd_f32_cl_q8.cu",
            "bwd_kernels.cu", "bwd_api.cu", "quant.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -289,13 +289,11 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     p.seg_len = pl.seg_len;
 
     const bool heads = a->a_heads > 0;
-    auto scan = [&](int what) {
-        if (es == 2)
-            return cl ? launch_scan_bwd_bf16_cl(what, pl.lanes, heads, p, s)
-                      : launch_scan_bwd_bf16(what, pl.lanes, heads, p, s);
-        return cl ? launch_scan_bwd_f32_cl(what, pl.lanes, heads, p, s)
-                  : launch_scan_bwd_f32(what, pl.lanes, heads, p, s);
-    };
+    using Launch = cudaError_t (*)(int, int, bool, const BwdParams&, cudaStream_t);
+    static constexpr Launch kLaunch[2][2][2] = {               // bf16?, channel-last?, 8 bits?
+        {{launch_scan_bwd_f32, launch_scan_bwd_f32_q8}, {launch_scan_bwd_f32_cl, launch_scan_bwd_f32_cl_q8}},
+        {{launch_scan_bwd_bf16, launch_scan_bwd_bf16_q8}, {launch_scan_bwd_bf16_cl, launch_scan_bwd_bf16_cl_q8}}};
+    auto scan = [&](int what) { return kLaunch[es == 2][cl][packed8](what, pl.lanes, heads, p, s); };
     if (a->seq_starts &&
         (e = launch_since(a->seq_starts, a->num_seqs, (int)L, ws + pl.since, s)) != cudaSuccess)
         return api_cuda(e, "sequence starts launch");

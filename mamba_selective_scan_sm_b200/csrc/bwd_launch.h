@@ -14,11 +14,13 @@ struct BwdVariant {
 };
 BwdVariant scan_bwd_variant(int lanes);
 
-// what: 0 checkpoints, 1 segment summaries, 2 the backward sweep.
-cudaError_t launch_scan_bwd_bf16(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st);
-cudaError_t launch_scan_bwd_f32(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st);
-cudaError_t launch_scan_bwd_bf16_cl(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st);
-cudaError_t launch_scan_bwd_f32_cl(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st);
+// what: 0 checkpoints, 1 segment summaries, 2 the backward sweep. One per activation type,
+// layout (_cl: channel-last) and form of u, delta and z (_q8: int8 codes).
+#define SSM_DECLARE_BWD(NAME_) \
+    cudaError_t launch_scan_bwd_##NAME_(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st);
+SSM_DECLARE_BWD(bf16) SSM_DECLARE_BWD(f32) SSM_DECLARE_BWD(bf16_cl) SSM_DECLARE_BWD(f32_cl)
+SSM_DECLARE_BWD(bf16_q8) SSM_DECLARE_BWD(f32_q8) SSM_DECLARE_BWD(bf16_cl_q8) SSM_DECLARE_BWD(f32_cl_q8)
+#undef SSM_DECLARE_BWD
 
 cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st);
 cudaError_t launch_scan_bwd_reduce(int elem_size, const BwdReduceParams& p, cudaStream_t st);

@@ -1,11 +1,11 @@
-// Instantiations of the backward scan kernels: f32 activations, channel-last layout.
+// Instantiations of the backward scan kernels: f32 activations, channel-last layout, plain u, delta, z.
 #define SSM_ERROR_WORD g_error_scan_bwd_f32_cl
 #include "scan_bwd_launch.cuh"
 
 namespace ssm {
 
 cudaError_t launch_scan_bwd_f32_cl(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st) {
-    return launch_scan_bwd_t<float, true>(what, lanes, heads, p, st);
+    return launch_scan_bwd_t<float, true, false>(what, lanes, heads, p, st);
 }
 
 }  // namespace ssm

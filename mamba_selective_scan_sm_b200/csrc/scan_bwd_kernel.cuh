@@ -29,6 +29,8 @@
 // in the same order every time.
 #pragma once
 
+#include <type_traits>
+
 #include "bwd_params.h"
 #include "device_common.cuh"
 
@@ -53,9 +55,11 @@ template <int S> struct BwdShape {
     // shared memory, in floats
     static constexpr int kSt = 4 * G * (TT + 1);               // {delta, delta, delta u, delta u}
     static constexpr int kG = 2 * G * (TT + 1);                // {g, g}
-    static constexpr int kU = G * (TT + 1);
-    static constexpr int kOut = G * (TT + 2);                  // one of y, s1, s2
-    static constexpr int kBC = NC * TT * RB;
+    static constexpr int RO = TT + 4;                          // row of u, y, s1, s2 in floats
+    static constexpr int kU = G * RO;
+    static constexpr int kOut = G * RO;                        // one of y, s1, s2
+    static constexpr int RQ = TT * RB + 16;                    // one order's copy of B / C: the copies
+    static constexpr int kBC = NC * RQ;                        // begin 16 banks apart
     static constexpr int kPart = kBwdWarps * TT * 2 * NS;
     static constexpr int kPrm = 8 * G;
     static constexpr int kMask = 4;                            // sequence starts of the tile, as bits
@@ -319,23 +323,23 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src, int have) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Rows of positions: `rows` rows (channels or states, those below `have` exist) of the TT
-// positions from pos0 on. unit: bytes per copy, a multiple of the element size e.
-template <int TT, int UNIT>
-__device__ __forceinline__ void fetch_rows(const uint8_t* src, int64_t sc, int e, int L, int pos0,
-                                           int rows, int have, uint8_t* dst, int drow) {
-    const int per = TT * e / UNIT;
-    for (int i = threadIdx.x; i < rows * per; i += kBwdThreads) {
+// Rows of positions: ROWS rows (channels or states, those below `have` exist) of the TT
+// positions from pos0 on, elements of E_ bytes, sc elements from row to row.
+template <int TT, int E_, int ROWS, int DROW>
+__device__ __forceinline__ void fetch_rows(const uint8_t* src, int64_t sc, int L, int pos0, int have, uint8_t* dst) {
+    constexpr int e = E_, UNIT = TT * e < 16 ? TT * e : 16, per = TT * e / UNIT, drow = DROW;
+#pragma unroll
+    for (int i = threadIdx.x; i < ROWS * per; i += kBwdThreads) {
         const int r = i / per, k = i % per, pos = pos0 + k * (UNIT / e);
         const bool in = r < have && pos >= 0 && pos < L;
         cp_async<UNIT>(dst + r * drow + k * UNIT, in ? src + ((int64_t)r * sc + pos) * e : src, in ? UNIT : 0);
     }
 }
-template <int TT>
-__device__ __forceinline__ void fetch_rows_slow(const uint8_t* src, int64_t sc, int e, int L, int pos0,
-                                                int rows, int have, uint8_t* dst, int drow) {
+template <int TT, int E_, int ROWS, int DROW>
+__device__ __noinline__ void fetch_rows_slow(const uint8_t* src, int64_t sc, int L, int pos0, int have, uint8_t* dst) {
+    constexpr int e = E_, drow = DROW;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < rows * TT; i += kBwdThreads) {
+    for (int i = threadIdx.x; i < ROWS * TT; i += kBwdThreads) {
         const int r = i / TT, k = i % TT, pos = pos0 + k;
         const bool in = r < have && pos >= 0 && pos < L;
         const uint8_t* q = src + ((int64_t)r * sc + pos) * e;
@@ -345,10 +349,12 @@ __device__ __forceinline__ void fetch_rows_slow(const uint8_t* src, int64_t sc, 
     }
 }
 // Channel-last rows: `have` elements of the steps t0 .. t0 + rows - 1 (scan order).
-__device__ __forceinline__ void fetch_steps(const uint8_t* src, int64_t sp, int e, int L, int t0, bool rev,
-                                            int rows, int width, int have, uint8_t* dst, int drow, bool async) {
+template <int E_, int WIDTH, int DROW>
+__device__ __forceinline__ void fetch_steps(const uint8_t* src, int64_t sp, int L, int t0, bool rev,
+                                            int rows, int have, uint8_t* dst, bool async) {
+    constexpr int e = E_, width = WIDTH, drow = DROW;
     if (async) {
-        const int per = (width * e + 15) / 16;
+        constexpr int per = (width * e + 15) / 16;
         for (int i = threadIdx.x; i < rows * per; i += kBwdThreads) {
             const int r = i / per, k = i % per, t = t0 + r, pos = rev ? L - 1 - t : t;
             const int n = t >= 0 && t < L ? min(16, max(0, have * e - 16 * k)) : 0;
@@ -370,41 +376,47 @@ __device__ __forceinline__ void fetch_steps(const uint8_t* src, int64_t sp, int 
 // Start copying the inputs of steps [t0, t0 + TT) into a buffer: x, delta, B, and with ADJ z,
 // dout, C. Asynchronous copies where the host found every row aligned to the copy unit
 // (p.async), else plain loads.
-template <typename T, int S, bool CL, bool ADJ>
+template <typename T, int S, bool CL, bool Q8, bool ADJ>
 __device__ __forceinline__ void fetch_tile(const BwdParams& p, int b, int d0, int t0, uint8_t* raw) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
     constexpr int TT = H::TT, ES = R::ES;
     const int L = p.seqlen, pos0 = p.reverse ? L - t0 - TT : t0, have = p.dim - d0;
-    const int eq = p.x.scale ? 1 : ES;                         // bytes per element of x, delta, z
+    constexpr int eq = Q8 ? 1 : ES;                            // bytes per element of x, delta, z
     auto base = [&](const void* q, const Str& st, int e) {
         return static_cast<const uint8_t*>(q) + ((int64_t)b * st.b + (int64_t)d0 * st.c) * e;
     };
-    auto rows = [&](const uint8_t* src, int64_t sc, int e, int n, int hv, uint8_t* dst, int drow) {
-        if (!p.async) fetch_rows_slow<TT>(src, sc, e, L, pos0, n, hv, dst, drow);
-        else if (e == 1 && TT == 8) fetch_rows<TT, 8>(src, sc, e, L, pos0, n, hv, dst, drow);
-        else fetch_rows<TT, 16>(src, sc, e, L, pos0, n, hv, dst, drow);
-    };
-    auto act = [&](const void* q, const Str& st, int e, uint8_t* dst) {
-        if constexpr (CL) fetch_steps(base(q, st, e), st.p, e, L, t0, p.reverse, TT, H::G, have, dst, R::kRow, p.async);
-        else rows(base(q, st, e), st.c, e, H::G, have, dst, R::kRow);
+    // x, delta or z (of eq bytes), dout (of ES)
+    auto act = [&](const void* q, const Str& st, auto size, uint8_t* dst) {
+        constexpr int e = decltype(size)::value;
+        if constexpr (CL) {
+            fetch_steps<e, H::G, R::kRow>(base(q, st, e), st.p, L, t0, p.reverse, TT, have, dst, p.async);
+        } else {
+            if (p.async) fetch_rows<TT, e, H::G, R::kRow>(base(q, st, e), st.c, L, pos0, have, dst);
+            else fetch_rows_slow<TT, e, H::G, R::kRow>(base(q, st, e), st.c, L, pos0, have, dst);
+        }
     };
     auto bc = [&](const void* q, const Str& st, uint8_t* dst) {
         const uint8_t* src = static_cast<const uint8_t*>(q) + (int64_t)b * st.b * ES;
-        if constexpr (CL) fetch_steps(src, st.p, ES, L, t0, p.reverse, TT, H::NS, p.dstate, dst, R::kBRow, p.async);
-        else rows(src, st.c, ES, H::NS, p.dstate, dst, R::kBRow);
+        if constexpr (CL) {
+            fetch_steps<ES, H::NS, R::kBRow>(src, st.p, L, t0, p.reverse, TT, p.dstate, dst, p.async);
+        } else {
+            if (p.async) fetch_rows<TT, ES, H::NS, R::kBRow>(src, st.c, L, pos0, p.dstate, dst);
+            else fetch_rows_slow<TT, ES, H::NS, R::kBRow>(src, st.c, L, pos0, p.dstate, dst);
+        }
     };
     const uint8_t* xb = base(p.x.p, p.x.s, eq);
     if constexpr (CL) {
         const int lead = p.conv_w ? 3 : 0;
-        fetch_steps(xb, p.x.s.p, eq, L, t0 - lead, p.reverse, TT + lead, H::G, have,
-                    raw + R::X + (3 - lead) * R::kXRow, R::kXRow, p.async);
+        fetch_steps<eq, H::G, R::kXRow>(xb, p.x.s.p, L, t0 - lead, p.reverse, TT + lead, have,
+                                        raw + R::X + (3 - lead) * R::kXRow, p.async);
     } else {
-        rows(xb, p.x.s.c, eq, H::G, have, raw + R::X + 16, R::kXRow);
+        if (p.async) fetch_rows<TT, eq, H::G, R::kXRow>(xb, p.x.s.c, L, pos0, have, raw + R::X + 16);
+        else fetch_rows_slow<TT, eq, H::G, R::kXRow>(xb, p.x.s.c, L, pos0, have, raw + R::X + 16);
         if (p.conv_w) {
             // the 4 or more positions the conv reads before the tile (reverse: behind it)
             if (p.async && eq * TT >= 16) {
-                const int he = 16 / eq;
+                constexpr int he = 16 / eq;
                 for (int r = threadIdx.x; r < H::G; r += kBwdThreads) {
                     const int pos = p.reverse ? pos0 + TT : pos0 - he;
                     const bool in = r < have && pos >= 0 && pos < L;
@@ -425,14 +437,16 @@ __device__ __forceinline__ void fetch_tile(const BwdParams& p, int b, int d0, in
             }
         }
     }
-    act(p.dt.p, p.dt.s, eq, raw + R::DT);
+    std::integral_constant<int, eq> in_size;
+    std::integral_constant<int, ES> full_size;
+    act(p.dt.p, p.dt.s, in_size, raw + R::DT);
     bc(p.Bm, p.sB, raw + R::B);
     if constexpr (ADJ) {
-        if (p.z.p) act(p.z.p, p.z.s, eq, raw + R::Z);
-        act(p.dy, p.sdy, ES, raw + R::DY);
+        if (p.z.p) act(p.z.p, p.z.s, in_size, raw + R::Z);
+        act(p.dy, p.sdy, full_size, raw + R::DY);
         bc(p.Cm, p.sC, raw + R::C);
     }
-    if (p.x.scale) {
+    if constexpr (Q8) {
         // a tile and its halo span at most two blocks of 64 positions: both their scales
         const int last = (L - 1) / kBlock8;
         const int lo = min(max(pos0 - 3, 0) / kBlock8, last), hi = min(max(pos0 + TT + 2, 0) / kBlock8, last);
@@ -473,14 +487,14 @@ __device__ __forceinline__ void take_run(const T* p, bool rev, float (&f)[N]) {
 
 // A thread's run of EPT values of x, delta or z (which = 0, 1, 2; codes where packed) or of
 // dout (which = 3), in scan order; for x shift steps earlier (channel-last only).
-template <typename T, int S, bool CL>
+template <typename T, int S, bool CL, bool Q8>
 __device__ __forceinline__ void take(const BwdParams& p, const uint8_t* raw, int which,
                                      const BwdRun<S, CL>& r, int t0, float (&f)[BwdShape<S>::EPT],
                                      int shift = 0) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
     constexpr int E = H::EPT;
-    const bool q8 = p.x.scale && which < 3, rev = !CL && p.reverse;
+    const bool q8 = Q8 && which < 3, rev = !CL && p.reverse;
     const uint8_t* row = raw + (which == 0 ? R::X + (CL ? (r.tl + 3 - shift) * R::kXRow : r.ch * R::kXRow + 16)
                                 : (which == 1 ? R::DT : which == 2 ? R::Z : R::DY) + (CL ? r.tl : r.ch) * R::kRow);
     const int at = CL ? r.ch : rev ? H::TT - E - r.tl : r.tl;
@@ -503,7 +517,7 @@ __device__ __forceinline__ void take(const BwdParams& p, const uint8_t* raw, int
 // the pairs they take) per channel and step, g and u where ADJ, and the rows of B (and C
 // where ADJ) in each order of the states. Steps past the end and channels past dim get
 // zeros: a = 1 and no input, which leave both recurrences where they are.
-template <typename T, int S, bool CL, bool ADJ>
+template <typename T, int S, bool CL, bool Q8, bool ADJ>
 __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, int t0, const uint8_t* raw,
                                            const float* prm, float4* st, float2* gs, float* us,
                                            float* Bs, float* Cs, uint32_t* mask) {
@@ -517,7 +531,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
     const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
     const uint8_t* since = raw + R::SINCE;
     float u[E], dt[E], g[E];
-    take<T, S, CL>(p, raw, 0, r, t0, u);
+    take<T, S, CL, Q8>(p, raw, 0, r, t0, u);
     if (p.conv_w) {
         float acc[E];
 #pragma unroll
@@ -536,7 +550,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
 #pragma unroll
             for (int lag = 1; lag < 4; ++lag) {
                 float x[E];
-                take<T, S, CL>(p, raw, 0, r, t0, x, lag);
+                take<T, S, CL, Q8>(p, raw, 0, r, t0, x, lag);
                 if (t - lag < 0)
 #pragma unroll
                     for (int i = 0; i < E; ++i) x[i] = past(r.ch + i, t - lag);
@@ -547,7 +561,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
         } else {
             float xh[3];                                       // the 3 steps before the run
             const uint8_t* row = raw + R::X + r.ch * R::kXRow;
-            const int eq = p.x.scale ? 1 : R::ES;
+            constexpr int eq = Q8 ? 1 : R::ES;
             const float* sc = reinterpret_cast<const float*>(raw + R::SC);
             const int pos0 = p.reverse ? L - t0 - H::TT : t0, blk0 = max(pos0 - 3, 0) / kBlock8;
 #pragma unroll
@@ -557,7 +571,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
                                       : p.reverse ? -1 - o : 16 / eq + o;
                 if (t0 + o < 0) {
                     xh[m] = past(r.ch, t0 + o);
-                } else if (p.x.scale) {
+                } else if (Q8) {
                     const int pos = p.reverse ? L - 1 - (t0 + o) : t0 + o;
                     xh[m] = (float)reinterpret_cast<const int8_t*>(row)[at] *
                             sc[(pos / kBlock8 == blk0 ? 0 : H::G) + r.ch];
@@ -581,12 +595,12 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
 #pragma unroll
         for (int i = 0; i < E; ++i) u[i] = silu(acc[i]);
     }
-    take<T, S, CL>(p, raw, 1, r, t0, dt);
+    take<T, S, CL, Q8>(p, raw, 1, r, t0, dt);
     if constexpr (ADJ) {
-        take<T, S, CL>(p, raw, 3, r, t0, g);
+        take<T, S, CL, Q8>(p, raw, 3, r, t0, g);
         if (p.z.p) {
             float z[E];
-            take<T, S, CL>(p, raw, 2, r, t0, z);
+            take<T, S, CL, Q8>(p, raw, 2, r, t0, z);
 #pragma unroll
             for (int i = 0; i < E; ++i) g[i] *= silu(z[i]);
         }
@@ -604,7 +618,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
         st[o] = make_float4(dl, dl, du, du);
         if constexpr (ADJ) {
             gs[o] = make_float2(g[i], g[i]);
-            us[o] = u[i];
+            us[r.c(i) * H::RO + r.t(i)] = u[i];
         }
     }
     if (tid < 32) {
@@ -612,19 +626,24 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
                                                           since[tid < H::TT ? tid : 0] == 0);
         if (tid == 0) *mask = m;
     }
-    // rows of B and C
-    const T* Br = reinterpret_cast<const T*>(raw + R::B);
-    const T* Cr = reinterpret_cast<const T*>(raw + R::C);
-#pragma unroll 4
-    for (int k = tid; k < H::NS * H::TT; k += kBwdThreads) {
-        const int n = k % H::NS, tl = k / H::NS;
-        const int at = CL ? tl * (R::kBRow / R::ES) + n : n * H::TT + (p.reverse ? H::TT - 1 - tl : tl);
-        const float bv = Elem<T>::to_f(Br[at]), cv = ADJ ? Elem<T>::to_f(Cr[at]) : 0.f;
+    // rows of B and C: the 4 states of a lane at a step, once per order
 #pragma unroll
-        for (int q = 0; q < H::NC; ++q) {
-            Bs[(q * H::TT + tl) * H::RB + (n ^ q)] = bv;
-            if constexpr (ADJ) Cs[(q * H::TT + tl) * H::RB + (n ^ q)] = cv;
+    for (int k = tid; k < S * H::TT * (ADJ ? 2 : 1); k += kBwdThreads) {
+        const int jj = k % S, tl = k / S % H::TT;
+        const bool isC = ADJ && k >= S * H::TT;
+        const T* src = reinterpret_cast<const T*>(raw + (isC ? R::C : R::B));
+        float v[4];
+        if constexpr (CL) {
+            take_run<T, 4>(src + tl * (R::kBRow / R::ES) + 4 * jj, false, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = Elem<T>::to_f(src[(4 * jj + i) * H::TT + (p.reverse ? H::TT - 1 - tl : tl)]);
         }
+        float* dst = (isC ? Cs : Bs) + tl * H::RB + 4 * jj;
+#pragma unroll
+        for (int q = 0; q < H::NC; ++q)
+            *reinterpret_cast<float4*>(dst + q * H::RQ) = make_float4(v[q], v[1 ^ q], v[2 ^ q], v[3 ^ q]);
     }
 }
 
@@ -705,7 +724,7 @@ __device__ __forceinline__ int64_t ns_off(const BwdParams& p, int64_t row, int d
 }
 
 // The forward pass: checkpoints of the state (MODE kCheckpoint), or a segment's summary.
-template <typename T, int S, bool CL, bool HEADS, int MODE>
+template <typename T, int S, bool CL, bool Q8, bool HEADS, int MODE>
 __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr bool SUM = MODE == kSummary;
@@ -736,13 +755,13 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
         if (!SUM && seg == 0) load_state<S>(p, p.h0, b, d, j, h[kc]);
         if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc]);
     }
-    fetch_tile<T, S, CL, SUM>(p, b, d0, tb, raw);
+    fetch_tile<T, S, CL, Q8, SUM>(p, b, d0, tb, raw);
     int buf = 0;
     for (int t0 = tb; t0 < te; t0 += H::TT, buf ^= 1) {
         cp_async_wait();
         __syncthreads();                                       // this tile is here, the last one used
-        if (t0 + H::TT < te) fetch_tile<T, S, CL, SUM>(p, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
-        stage_tile<T, S, CL, SUM>(p, b, d0, t0, raw + buf * kRaw, prm, st, gs, us, Bs, Cs, mask);
+        if (t0 + H::TT < te) fetch_tile<T, S, CL, Q8, SUM>(p, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
+        stage_tile<T, S, CL, Q8, SUM>(p, b, d0, t0, raw + buf * kRaw, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
         const uint32_t starts = *mask;
 #pragma unroll
@@ -753,8 +772,8 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
                 if (!SUM && d < p.dim)
                     stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / kSubSteps + sub, d, j), h[kc]);
                 const int o = c * (H::TT + 1) + sub * kSubSteps;
-                const float* Br = Bs + (q * H::TT + sub * kSubSteps) * H::RB + 4 * j;
-                const float* Cr = Cs + (q * H::TT + sub * kSubSteps) * H::RB + 4 * j;
+                const float* Br = Bs + q * H::RQ + sub * kSubSteps * H::RB + 4 * j;
+                const float* Cr = Cs + q * H::RQ + sub * kSubSteps * H::RB + 4 * j;
                 uint64_t a[kSubSteps][2], du2[kSubSteps];
                 decays<HEADS>(A2[kc], st + o, starts >> (sub * kSubSteps) & 255, a, du2);
 #pragma unroll
@@ -818,7 +837,7 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
 }
 
 // The backward sweep.
-template <typename T, int S, bool CL, bool HEADS>
+template <typename T, int S, bool CL, bool Q8, bool HEADS>
 __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr int KC = H::KC, TT = H::TT, E = H::EPT;
@@ -877,15 +896,15 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
     };
     uint64_t hn[2] = {0, 0};
     load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
-    fetch_tile<T, S, CL, true>(p, b, d0, tb + (ntiles - 1) * TT, raw);
+    fetch_tile<T, S, CL, Q8, true>(p, b, d0, tb + (ntiles - 1) * TT, raw);
     int buf = 0;
     for (int tile = ntiles - 1; tile >= 0; --tile, buf ^= 1) {
         const int t0 = tb + tile * TT;
         const uint8_t* cur = raw + buf * kRaw;
         cp_async_wait();
         __syncthreads();                                       // this tile is here, the last one used
-        if (tile > 0) fetch_tile<T, S, CL, true>(p, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
-        stage_tile<T, S, CL, true>(p, b, d0, t0, cur, prm, st, gs, us, Bs, Cs, mask);
+        if (tile > 0) fetch_tile<T, S, CL, Q8, true>(p, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
+        stage_tile<T, S, CL, Q8, true>(p, b, d0, t0, cur, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
         const uint32_t starts = *mask;
 #pragma unroll 1
@@ -911,8 +930,8 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                     ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
                 }
                 const int so = c * (TT + 1) + sub * kSubSteps;
-                const float* Br = Bs + (sq * TT + sub * kSubSteps) * H::RB + 4 * j;
-                const float* Cr = Cs + (sq * TT + sub * kSubSteps) * H::RB + 4 * j;
+                const float* Br = Bs + sq * H::RQ + sub * kSubSteps * H::RB + 4 * j;
+                const float* Cr = Cs + sq * H::RQ + sub * kSubSteps * H::RB + 4 * j;
                 uint64_t a[kSubSteps][2], h[kSubSteps][2];
                 {
                     uint64_t du2[kSubSteps];
@@ -967,7 +986,7 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                 reduce8<S>(s1, lane);
                 reduce8<S>(s2, lane);
                 if (j < 8) {
-                    const int o = c * (TT + 2) + sub * kSubSteps + reduce8_first<S>(lane);
+                    const int o = c * H::RO + sub * kSubSteps + reduce8_first<S>(lane);
                     constexpr int CNT = S >= 8 ? 1 : 8 / S;
 #pragma unroll
                     for (int k = 0; k < CNT; ++k) {
@@ -1011,17 +1030,17 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
             const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
             if (hi > 0) {
                 float dt[E], z[E], dy[E], du[E], ddt[E], dz[E];
-                take<T, S, CL>(p, cur, 1, run, t0, dt);
+                take<T, S, CL, Q8>(p, cur, 1, run, t0, dt);
                 if (p.z.p) {
-                    take<T, S, CL>(p, cur, 2, run, t0, z);
-                    take<T, S, CL>(p, cur, 3, run, t0, dy);
+                    take<T, S, CL, Q8>(p, cur, 2, run, t0, z);
+                    take<T, S, CL, Q8>(p, cur, 3, run, t0, dy);
                 }
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    const int c = run.c(i), tl = run.t(i), o = c * (TT + 2) + tl;
+                    const int c = run.c(i), tl = run.t(i), o = c * H::RO + tl;
                     const float4 s = st[c * (TT + 1) + tl];
                     const float g = gs[c * (TT + 1) + tl].x;
-                    const float u = us[c * (TT + 1) + tl], Dv = prm[c * 8 + 6];
+                    const float u = us[o], Dv = prm[c * 8 + 6];
                     const float s1 = s1s[o], s2 = s2s[o] * kLn2;
                     du[i] = fmaf(g, Dv, s.x * s1);
                     const float ddelta = fmaf(u, s1, s2);
@@ -1056,11 +1075,19 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
             constexpr int ROW = 2 * H::NS;
             float* out = p.parts + (((int64_t)blockIdx.x * p.batch + b) * L + t0) * ROW;
             const int n = min(TT, te - t0) * ROW;
-            for (int k = tid; k < n; k += kBwdThreads) {
-                float v = part[k];
 #pragma unroll
-                for (int w = 1; w < kBwdWarps; ++w) v += part[w * TT * ROW + k];
-                out[k] = v;
+            for (int k = tid * 4; k < TT * ROW; k += kBwdThreads * 4) {
+                if (k >= n) break;
+                float4 v = *reinterpret_cast<const float4*>(part + k);
+#pragma unroll
+                for (int w = 1; w < kBwdWarps; ++w) {
+                    const float4 q = *reinterpret_cast<const float4*>(part + w * TT * ROW + k);
+                    v.x += q.x;
+                    v.y += q.y;
+                    v.z += q.z;
+                    v.w += q.w;
+                }
+                *reinterpret_cast<float4*>(out + k) = v;
             }
         }
     }

@@ -17,29 +17,29 @@ inline cudaError_t launch_with_smem(K k, dim3 grid, int smem, const BwdParams& p
     return cudaGetLastError();
 }
 
-template <typename T, int S, bool CL, bool HEADS>
+template <typename T, int S, bool CL, bool Q8, bool HEADS>
 inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t st) {
     using H = BwdShape<S>;
     constexpr int kRaw = 2 * BwdRaw<T, S, CL>::BYTES;
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
-        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, HEADS, kCheckpoint>, grid,
+        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid,
                                 (H::kSt + H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
     if (what == 1)
-        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, HEADS, kSummary>, grid,
+        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kSummary>, grid,
                                 (H::kSt + H::kG + H::kU + 2 * H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
-    return launch_with_smem(scan_bwd_kernel<T, S, CL, HEADS>, grid,
+    return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid,
                             (H::kSt + H::kG + H::kU + 3 * H::kOut + 2 * H::kBC + H::kPart + H::kPrm +
                              H::kMask + H::kCarry + (CL ? H::kSum : 0)) * 4 + kRaw,
                             p, st);
 }
 
-template <typename T, bool CL>
+template <typename T, bool CL, bool Q8>
 inline cudaError_t launch_scan_bwd_t(int what, int lanes, bool heads, const BwdParams& p, cudaStream_t st) {
 #define SSM_BWD(S_)                                                                           \
     if (lanes == S_)                                                                          \
-        return heads ? launch_scan_bwd_v<T, S_, CL, true>(what, p, st)                        \
-                     : launch_scan_bwd_v<T, S_, CL, false>(what, p, st);
+        return heads ? launch_scan_bwd_v<T, S_, CL, Q8, true>(what, p, st)                        \
+                     : launch_scan_bwd_v<T, S_, CL, Q8, false>(what, p, st);
     SSM_BWD(1) SSM_BWD(2) SSM_BWD(4) SSM_BWD(8) SSM_BWD(16) SSM_BWD(32)
 #undef SSM_BWD
     return cudaErrorInvalidValue;

@@ -276,6 +276,11 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     p.dz = a->dz;
     p.sddt = str(a->stride_ddelta, D);
     p.sdz = str(a->stride_dz, D);
+    // A thread's outputs are runs of up to 16 bytes (fp32: 32), from multiples of their length.
+    bool vec = is_aligned(a->du, 16) && is_aligned(a->ddelta, 16) && is_aligned(a->dz, 16);
+    if (cl) vec = vec && p.sdu.p % 8 == 0 && p.sddt.p % 8 == 0 && (!a->dz || p.sdz.p % 8 == 0);
+    else vec = vec && L % 8 == 0;
+    p.vec_out = vec ? 1 : 0;
     p.dh0 = a->dinitial_state;
     p.ckpt = f(pl.ckpt);
     p.nsub = pl.nsub;

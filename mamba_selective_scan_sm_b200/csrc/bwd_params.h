@@ -32,6 +32,7 @@ struct BwdParams {
     const float *D, *dbias, *conv_w, *conv_b;
     int conv_width, softplus, reverse, head_dim;
     int async;                    // every row is aligned to the asynchronous copies' unit
+    int vec_out;                  // the outputs' runs are aligned to 16 bytes
     const float* h0;              // (batch, dim, dstate) or null
     const float* dhl;             // (batch, dim, dstate) or null: gradient of the last state
     const void* hist;             // (batch, dim, conv_width - 1) or null

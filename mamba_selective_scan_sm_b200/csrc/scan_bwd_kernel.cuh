@@ -80,8 +80,9 @@ __device__ __forceinline__ int slot_order(int d) {
 }
 
 // One tile's inputs as they lie in global memory, copied to shared memory a tile ahead of
-// their use (two buffers): rows of positions (x with the copy unit before it for the conv),
-// or channel-last rows of channels in scan order (x with 3 steps before it).
+// their use (two buffers): rows of positions (x with a halo for the conv in front, or behind
+// in the reverse direction), or channel-last rows of channels in scan order (x with 3 steps
+// before it).
 template <typename T, int S, bool CL> struct BwdRaw {
     using H = BwdShape<S>;
     static constexpr int ES = (int)sizeof(T);
@@ -315,141 +316,182 @@ __device__ __forceinline__ void load_prm(const BwdParams& p, int d0, float* prm)
 }
 
 template <int BYTES>
-__device__ __forceinline__ void cp_async(void* dst, const void* src, int have) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int have) {
     // BYTES (4, 8 or 16) to shared memory, the first `have` of them from src, zeros behind
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
                  "r"(have));
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Rows of positions: ROWS rows (channels or states, those below `have` exist) of the TT
-// positions from pos0 on, elements of E_ bytes, sc elements from row to row.
-template <int TT, int E_, int ROWS, int DROW>
-__device__ __forceinline__ void fetch_rows(const uint8_t* src, int64_t sc, int L, int pos0, int have, uint8_t* dst) {
-    constexpr int e = E_, UNIT = TT * e < 16 ? TT * e : 16, per = TT * e / UNIT, drow = DROW;
-#pragma unroll
-    for (int i = threadIdx.x; i < ROWS * per; i += kBwdThreads) {
-        const int r = i / per, k = i % per, pos = pos0 + k * (UNIT / e);
-        const bool in = r < have && pos >= 0 && pos < L;
-        cp_async<UNIT>(dst + r * drow + k * UNIT, in ? src + ((int64_t)r * sc + pos) * e : src, in ? UNIT : 0);
-    }
-}
-template <int TT, int E_, int ROWS, int DROW>
-__device__ __noinline__ void fetch_rows_slow(const uint8_t* src, int64_t sc, int L, int pos0, int have, uint8_t* dst) {
-    constexpr int e = E_, drow = DROW;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < ROWS * TT; i += kBwdThreads) {
-        const int r = i / TT, k = i % TT, pos = pos0 + k;
-        const bool in = r < have && pos >= 0 && pos < L;
-        const uint8_t* q = src + ((int64_t)r * sc + pos) * e;
-        if (e == 4) reinterpret_cast<uint32_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-        else if (e == 2) reinterpret_cast<uint16_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
-        else (dst + r * drow)[k] = in ? *q : 0;
-    }
-}
-// Channel-last rows: `have` elements of the steps t0 .. t0 + rows - 1 (scan order).
-template <int E_, int WIDTH, int DROW>
-__device__ __forceinline__ void fetch_steps(const uint8_t* src, int64_t sp, int L, int t0, bool rev,
-                                            int rows, int have, uint8_t* dst, bool async) {
-    constexpr int e = E_, width = WIDTH, drow = DROW;
-    if (async) {
-        constexpr int per = (width * e + 15) / 16;
-        for (int i = threadIdx.x; i < rows * per; i += kBwdThreads) {
-            const int r = i / per, k = i % per, t = t0 + r, pos = rev ? L - 1 - t : t;
-            const int n = t >= 0 && t < L ? min(16, max(0, have * e - 16 * k)) : 0;
-            cp_async<16>(dst + r * drow + k * 16, n ? src + (int64_t)pos * sp * e + k * 16 : src, n);
+// One asynchronous copy of a tile, worked out once: its source advances with the tile.
+struct __align__(16) BwdCopy {
+    const uint8_t* src;           // the row (position 0), or channel-last the unit of the row
+    uint32_t step;                // channel-last: bytes between positions / 16; else log2 of the element size
+    uint16_t dst;                 // in the buffer
+    int8_t at;                    // position relative to the tile's lowest, or step to its first
+    int8_t bytes;                 // that exist (zeros are filled in behind); < 0: no copy
+};
+
+template <typename T, int S, bool CL, bool Q8, bool ADJ> struct BwdCopies {
+    using H = BwdShape<S>;
+    using R = BwdRaw<T, S, CL>;
+    static constexpr int TT = H::TT, ES = R::ES, EQ = Q8 ? 1 : ES;     // EQ: of x, delta, z
+    // bytes of a copy and copies of a row, for rows of x, delta, z (Q), dout and B, C
+    static constexpr int UQ = !CL && TT * EQ < 16 ? TT * EQ : 16;
+    static constexpr int PQ = CL ? H::G * EQ / 16 : TT * EQ / UQ;
+    static constexpr int PY = CL ? H::G * ES / 16 : TT * ES / 16;
+    static constexpr int PB = CL ? (H::NS * ES + 15) / 16 : TT * ES / 16;
+    static constexpr int NX = CL ? (TT + 3) * PQ : H::G * PQ;
+    static constexpr int NQ = CL ? TT * PQ : H::G * PQ;
+    static constexpr int NH = CL ? 0 : H::G;                           // halos of x
+    static constexpr int NB = CL ? TT * PB : H::NS * PB;
+    static constexpr int NY = CL ? TT * PY : H::G * PY;
+    // x, halo, delta, B (and with ADJ z, dout, C)
+    static constexpr int COUNT = NX + NH + NQ + NB + (ADJ ? NQ + NY + NB : 0);
+    static constexpr int PER = (COUNT + kBwdThreads - 1) / kBwdThreads;
+
+    static __device__ BwdCopy make(const BwdParams& p, int b, int d0, int id) {
+        const int have = p.dim - d0;
+        auto rows = [&](const void* q, const Str& st, int first, int count, int e, int unit, int per, int i,
+                        int off, int drow) {
+            // positions of row i / per
+            const int r = i / per, k = i % per;
+            const uint8_t* src = static_cast<const uint8_t*>(q) + ((int64_t)b * st.b + (int64_t)(first + (r < count ? r : 0)) * st.c) * e;
+            return BwdCopy{src, (uint32_t)(e == 4 ? 2 : e - 1), (uint16_t)(off + r * drow + k * unit),
+                           (int8_t)(k * (unit / e)), (int8_t)(r < count ? unit : 0)};
+        };
+        auto steps = [&](const void* q, const Str& st, int first, int count, int e, int per, int i, int lead,
+                         int off, int drow) {
+            const int r = i / per, k = i % per;
+            const uint8_t* src = static_cast<const uint8_t*>(q) + ((int64_t)b * st.b + first) * e + k * 16;
+            const int n = min(16, max(0, count * e - 16 * k));
+            return BwdCopy{src, (uint32_t)(st.p * e / 16), (uint16_t)(off + r * drow + k * 16),
+                           (int8_t)(r - lead), (int8_t)n};
+        };
+        auto act = [&](const ActIn& a, int i, int off) {
+            if constexpr (CL) return steps(a.p, a.s, d0, have, EQ, PQ, i, 0, off, R::kRow);
+            else return rows(a.p, a.s, d0, have, EQ, UQ, PQ, i, off, R::kRow);
+        };
+        auto bc = [&](const void* q, const Str& st, int i, int off) {
+            if constexpr (CL) return steps(q, st, 0, p.dstate, ES, PB, i, 0, off, R::kBRow);
+            else return rows(q, st, 0, p.dstate, ES, 16, PB, i, off, R::kBRow);
+        };
+        const BwdCopy none{nullptr, 0, 0, 0, -1};
+        if (id < NX) {
+            if constexpr (CL) {
+                return id / PQ < 3 && !p.conv_w ? none : steps(p.x.p, p.x.s, d0, have, EQ, PQ, id, 3, R::X, R::kXRow);
+            } else {
+                return rows(p.x.p, p.x.s, d0, have, EQ, UQ, PQ, id, R::X + (p.reverse ? 0 : 16), R::kXRow);
+            }
         }
-        return;
+        id -= NX;
+        if (id < NH) {
+            if (!p.conv_w) return none;
+            BwdCopy c = rows(p.x.p, p.x.s, d0, have, EQ, UQ, 1, id, R::X + (p.reverse ? TT * EQ : 16 - UQ), R::kXRow);
+            c.at = (int8_t)(p.reverse ? TT : -(UQ / EQ));
+            return c;
+        }
+        id -= NH;
+        if (id < NQ) return act(p.dt, id, R::DT);
+        id -= NQ;
+        if (id < NB) return bc(p.Bm, p.sB, id, R::B);
+        id -= NB;
+        if (!ADJ) return none;
+        if (id < NQ) return p.z.p ? act(p.z, id, R::Z) : none;
+        id -= NQ;
+        if (id < NY) {
+            if constexpr (CL) return steps(p.dy, p.sdy, d0, have, ES, PY, id, 0, R::DY, R::kRow);
+            else return rows(p.dy, p.sdy, d0, have, ES, 16, PY, id, R::DY, R::kRow);
+        }
+        id -= NY;
+        return id < NB ? bc(p.Cm, p.sC, id, R::C) : none;
     }
-#pragma unroll 4
-    for (int i = threadIdx.x; i < rows * width; i += kBwdThreads) {
-        const int r = i / width, k = i % width, t = t0 + r, pos = rev ? L - 1 - t : t;
-        const bool in = t >= 0 && t < L && k < have;
-        const uint8_t* q = src + ((int64_t)pos * sp + k) * e;
-        if (e == 4) reinterpret_cast<uint32_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-        else if (e == 2) reinterpret_cast<uint16_t*>(dst + r * drow)[k] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
-        else (dst + r * drow)[k] = in ? *q : 0;
+};
+
+// The plain form of the same copies, element by element, for rows that are not aligned.
+template <typename T, int S, bool CL, bool Q8, bool ADJ>
+__device__ __forceinline__ void fetch_plain(const BwdParams& p, int b, int d0, int t0, uint8_t* raw) {
+    using H = BwdShape<S>;
+    using R = BwdRaw<T, S, CL>;
+    constexpr int TT = H::TT, ES = R::ES, EQ = Q8 ? 1 : ES;
+    const int L = p.seqlen, pos0 = p.reverse ? L - t0 - TT : t0, have = p.dim - d0;
+    auto put = [&](uint8_t* dst, int k, const uint8_t* q, bool in, auto size) {
+        constexpr int e = decltype(size)::value;
+        if constexpr (e == 4) reinterpret_cast<uint32_t*>(dst)[k] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+        else if constexpr (e == 2) reinterpret_cast<uint16_t*>(dst)[k] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
+        else dst[k] = in ? *q : 0;
+    };
+    // `rows` rows of `width` elements; which of a row and its column is the position goes by CL
+    auto copy = [&](const void* ptr, const Str& st, int first, int count, int rows, int width, int lead,
+                    uint8_t* dst, int drow, auto size) {
+        constexpr int e = decltype(size)::value;
+        const uint8_t* src = static_cast<const uint8_t*>(ptr) + (int64_t)b * st.b * e;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < rows * width; i += kBwdThreads) {
+            const int r = i / width, k = i % width, t = t0 - lead + r;
+            const int pos = CL ? (p.reverse ? L - 1 - t : t) : pos0 + k, c = CL ? k : r;
+            const bool in = c < count && pos >= 0 && pos < L;
+            put(dst + r * drow, k, src + ((int64_t)(first + c) * st.c + (int64_t)pos * st.p) * e, in, size);
+        }
+    };
+    std::integral_constant<int, EQ> sq;
+    std::integral_constant<int, ES> se;
+    constexpr int ROWS = CL ? TT : H::G, WIDTH = CL ? H::G : TT;
+    if constexpr (CL) {
+        copy(p.x.p, p.x.s, d0, have, TT + 3, H::G, 3, raw + R::X, R::kXRow, sq);
+    } else {
+        copy(p.x.p, p.x.s, d0, have, H::G, TT, 0, raw + R::X + (p.reverse ? 0 : 16), R::kXRow, sq);
+        const uint8_t* src = static_cast<const uint8_t*>(p.x.p) + ((int64_t)b * p.x.s.b + (int64_t)d0 * p.x.s.c) * EQ;
+        for (int i = threadIdx.x; i < (p.conv_w ? H::G * 4 : 0); i += kBwdThreads) {
+            const int r = i / 4, o = i % 4 - 4, t = t0 + o, pos = p.reverse ? L - 1 - t : t;
+            put(raw + R::X + r * R::kXRow, p.reverse ? TT - 1 - o : 16 / EQ + o,
+                src + ((int64_t)r * p.x.s.c + pos) * EQ, r < have && pos >= 0 && pos < L, sq);
+        }
+    }
+    copy(p.dt.p, p.dt.s, d0, have, ROWS, WIDTH, 0, raw + R::DT, R::kRow, sq);
+    copy(p.Bm, p.sB, 0, p.dstate, CL ? TT : H::NS, CL ? H::NS : TT, 0, raw + R::B, R::kBRow, se);
+    if constexpr (ADJ) {
+        if (p.z.p) copy(p.z.p, p.z.s, d0, have, ROWS, WIDTH, 0, raw + R::Z, R::kRow, sq);
+        copy(p.dy, p.sdy, d0, have, ROWS, WIDTH, 0, raw + R::DY, R::kRow, se);
+        copy(p.Cm, p.sC, 0, p.dstate, CL ? TT : H::NS, CL ? H::NS : TT, 0, raw + R::C, R::kBRow, se);
     }
 }
 
 // Start copying the inputs of steps [t0, t0 + TT) into a buffer: x, delta, B, and with ADJ z,
-// dout, C. Asynchronous copies where the host found every row aligned to the copy unit
-// (p.async), else plain loads.
+// dout, C. Asynchronous copies where the host found every row aligned to their units
+// (p.async), from the CTA's table; else plain loads.
 template <typename T, int S, bool CL, bool Q8, bool ADJ>
-__device__ __forceinline__ void fetch_tile(const BwdParams& p, int b, int d0, int t0, uint8_t* raw) {
+__device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* table, int b, int d0, int t0,
+                                           uint8_t* raw) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
-    constexpr int TT = H::TT, ES = R::ES;
-    const int L = p.seqlen, pos0 = p.reverse ? L - t0 - TT : t0, have = p.dim - d0;
-    constexpr int eq = Q8 ? 1 : ES;                            // bytes per element of x, delta, z
-    auto base = [&](const void* q, const Str& st, int e) {
-        return static_cast<const uint8_t*>(q) + ((int64_t)b * st.b + (int64_t)d0 * st.c) * e;
-    };
-    // x, delta or z (of eq bytes), dout (of ES)
-    auto act = [&](const void* q, const Str& st, auto size, uint8_t* dst) {
-        constexpr int e = decltype(size)::value;
-        if constexpr (CL) {
-            fetch_steps<e, H::G, R::kRow>(base(q, st, e), st.p, L, t0, p.reverse, TT, have, dst, p.async);
-        } else {
-            if (p.async) fetch_rows<TT, e, H::G, R::kRow>(base(q, st, e), st.c, L, pos0, have, dst);
-            else fetch_rows_slow<TT, e, H::G, R::kRow>(base(q, st, e), st.c, L, pos0, have, dst);
+    using K = BwdCopies<T, S, CL, Q8, ADJ>;
+    const int L = p.seqlen, pos0 = p.reverse ? L - t0 - H::TT : t0;
+    if (p.async) {
+        const uint32_t dst = smem_u32(raw);
+#pragma unroll
+        for (int k = 0; k < K::PER; ++k) {
+            const int id = threadIdx.x + k * kBwdThreads;
+            if (id >= K::COUNT) break;
+            const BwdCopy c = table[id];
+            const int pos = CL ? (p.reverse ? L - 1 - (t0 + c.at) : t0 + c.at) : pos0 + c.at;
+            const int n = pos >= 0 && pos < L ? c.bytes : 0;
+            const uint8_t* src = c.src + (n <= 0 ? 0 : CL ? (int64_t)pos * c.step * 16 : (int64_t)pos << c.step);
+            if (c.bytes < 0) continue;
+            // units of 8 bytes are those of 8-bit rows in 8-step tiles
+            if (K::UQ == 8 && id < K::NX + K::NH + K::NQ) cp_async<8>(dst + c.dst, src, n);
+            else if (K::UQ == 8 && ADJ && id >= K::NX + K::NH + K::NQ + K::NB && id < K::NX + K::NH + 2 * K::NQ + K::NB)
+                cp_async<8>(dst + c.dst, src, n);
+            else cp_async<16>(dst + c.dst, src, n);
         }
-    };
-    auto bc = [&](const void* q, const Str& st, uint8_t* dst) {
-        const uint8_t* src = static_cast<const uint8_t*>(q) + (int64_t)b * st.b * ES;
-        if constexpr (CL) {
-            fetch_steps<ES, H::NS, R::kBRow>(src, st.p, L, t0, p.reverse, TT, p.dstate, dst, p.async);
-        } else {
-            if (p.async) fetch_rows<TT, ES, H::NS, R::kBRow>(src, st.c, L, pos0, p.dstate, dst);
-            else fetch_rows_slow<TT, ES, H::NS, R::kBRow>(src, st.c, L, pos0, p.dstate, dst);
-        }
-    };
-    const uint8_t* xb = base(p.x.p, p.x.s, eq);
-    if constexpr (CL) {
-        const int lead = p.conv_w ? 3 : 0;
-        fetch_steps<eq, H::G, R::kXRow>(xb, p.x.s.p, L, t0 - lead, p.reverse, TT + lead, have,
-                                        raw + R::X + (3 - lead) * R::kXRow, p.async);
     } else {
-        if (p.async) fetch_rows<TT, eq, H::G, R::kXRow>(xb, p.x.s.c, L, pos0, have, raw + R::X + 16);
-        else fetch_rows_slow<TT, eq, H::G, R::kXRow>(xb, p.x.s.c, L, pos0, have, raw + R::X + 16);
-        if (p.conv_w) {
-            // the 4 or more positions the conv reads before the tile (reverse: behind it)
-            if (p.async && eq * TT >= 16) {
-                constexpr int he = 16 / eq;
-                for (int r = threadIdx.x; r < H::G; r += kBwdThreads) {
-                    const int pos = p.reverse ? pos0 + TT : pos0 - he;
-                    const bool in = r < have && pos >= 0 && pos < L;
-                    cp_async<16>(raw + R::X + r * R::kXRow, in ? xb + ((int64_t)r * p.x.s.c + pos) * eq : xb, in ? 16 : 0);
-                }
-            } else {
-                for (int i = threadIdx.x; i < H::G * 3; i += kBwdThreads) {
-                    // scan offsets -3 .. -1, in the places the copy above would put them
-                    const int r = i / 3, o = i % 3 - 3, t = t0 + o, pos = p.reverse ? L - 1 - t : t;
-                    const int at = p.reverse ? -1 - o : 16 / eq + o;
-                    const bool in = r < have && t >= 0 && t < L;
-                    const uint8_t* q = xb + ((int64_t)r * p.x.s.c + pos) * eq;
-                    uint8_t* dst = raw + R::X + r * R::kXRow;
-                    if (eq == 4) reinterpret_cast<uint32_t*>(dst)[at] = in ? *reinterpret_cast<const uint32_t*>(q) : 0u;
-                    else if (eq == 2) reinterpret_cast<uint16_t*>(dst)[at] = in ? *reinterpret_cast<const uint16_t*>(q) : 0;
-                    else dst[at] = in ? *q : 0;
-                }
-            }
-        }
-    }
-    std::integral_constant<int, eq> in_size;
-    std::integral_constant<int, ES> full_size;
-    act(p.dt.p, p.dt.s, in_size, raw + R::DT);
-    bc(p.Bm, p.sB, raw + R::B);
-    if constexpr (ADJ) {
-        if (p.z.p) act(p.z.p, p.z.s, in_size, raw + R::Z);
-        act(p.dy, p.sdy, full_size, raw + R::DY);
-        bc(p.Cm, p.sC, raw + R::C);
+        fetch_plain<T, S, CL, Q8, ADJ>(p, b, d0, t0, raw);
     }
     if constexpr (Q8) {
         // a tile and its halo span at most two blocks of 64 positions: both their scales
-        const int last = (L - 1) / kBlock8;
-        const int lo = min(max(pos0 - 3, 0) / kBlock8, last), hi = min(max(pos0 + TT + 2, 0) / kBlock8, last);
+        const int have = p.dim - d0, last = (L - 1) / kBlock8;
+        const int lo = min(max(pos0 - 3, 0) / kBlock8, last), hi = min(max(pos0 + H::TT + 2, 0) / kBlock8, last);
         for (int i = threadIdx.x; i < 6 * H::G; i += kBwdThreads) {
             const int c = i % H::G, which = i / H::G, k = which / 2;
             const ActIn& a = k == 0 ? p.x : k == 1 ? p.dt : p.z;
@@ -457,10 +499,10 @@ __device__ __forceinline__ void fetch_tile(const BwdParams& p, int b, int d0, in
             const float* q = in ? a.scale + (int64_t)b * a.ss.b + (int64_t)(d0 + c) * a.ss.c +
                                       (int64_t)(which % 2 ? hi : lo) * a.ss.p
                                 : p.x.scale;
-            cp_async<4>(raw + R::SC + 4 * i, q, in ? 4 : 0);
+            cp_async<4>(smem_u32(raw + R::SC + 4 * i), q, in ? 4 : 0);
         }
     }
-    if (p.since && threadIdx.x == 0) cp_async<TT>(raw + R::SINCE, p.since + t0, TT);
+    if (p.since && threadIdx.x == 0) cp_async<H::TT>(smem_u32(raw + R::SINCE), p.since + t0, H::TT);
     cp_async_commit();
 }
 
@@ -485,6 +527,28 @@ __device__ __forceinline__ void take_run(const T* p, bool rev, float (&f)[N]) {
     }
 }
 
+// The first hi values of a run, to p (dense): from p on, or (rev) from p + N - 1 backwards.
+// vec: such runs are aligned to their size.
+template <typename T, int N>
+__device__ __forceinline__ void put_run(T* p, bool rev, bool vec, int hi, const float (&f)[N]) {
+    constexpr int BY = N * (int)sizeof(T), V = BY >= 16 ? 16 : BY;
+    if (vec && hi == N) {
+        alignas(16) T e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = Elem<T>::from_f(rev ? f[N - 1 - i] : f[i]);
+#pragma unroll
+        for (int k = 0; k < BY / V; ++k) {
+            if constexpr (V == 16) reinterpret_cast<uint4*>(p)[k] = reinterpret_cast<uint4*>(e)[k];
+            else if constexpr (V == 8) reinterpret_cast<uint2*>(p)[k] = reinterpret_cast<uint2*>(e)[k];
+            else reinterpret_cast<uint32_t*>(p)[k] = reinterpret_cast<uint32_t*>(e)[k];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < hi) p[rev ? N - 1 - i : i] = Elem<T>::from_f(f[i]);
+}
+
 // A thread's run of EPT values of x, delta or z (which = 0, 1, 2; codes where packed) or of
 // dout (which = 3), in scan order; for x shift steps earlier (channel-last only).
 template <typename T, int S, bool CL, bool Q8>
@@ -495,7 +559,7 @@ __device__ __forceinline__ void take(const BwdParams& p, const uint8_t* raw, int
     using R = BwdRaw<T, S, CL>;
     constexpr int E = H::EPT;
     const bool q8 = Q8 && which < 3, rev = !CL && p.reverse;
-    const uint8_t* row = raw + (which == 0 ? R::X + (CL ? (r.tl + 3 - shift) * R::kXRow : r.ch * R::kXRow + 16)
+    const uint8_t* row = raw + (which == 0 ? R::X + (CL ? (r.tl + 3 - shift) * R::kXRow : r.ch * R::kXRow + (p.reverse ? 0 : 16))
                                 : (which == 1 ? R::DT : which == 2 ? R::Z : R::DY) + (CL ? r.tl : r.ch) * R::kRow);
     const int at = CL ? r.ch : rev ? H::TT - E - r.tl : r.tl;
     if (!q8) {
@@ -559,36 +623,44 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
                     for (int i = 0; i < E; ++i) acc[i] = fmaf(prm[r.c(i) * 8 + 3 - lag], x[i], acc[i]);
             }
         } else {
-            float xh[3];                                       // the 3 steps before the run
+            float xh[3], h0[2], h1[2];                         // the 3 steps before the run
             const uint8_t* row = raw + R::X + r.ch * R::kXRow;
-            constexpr int eq = Q8 ? 1 : R::ES;
-            const float* sc = reinterpret_cast<const float*>(raw + R::SC);
-            const int pos0 = p.reverse ? L - t0 - H::TT : t0, blk0 = max(pos0 - 3, 0) / kBlock8;
+            using Q = std::conditional_t<Q8, int8_t, T>;
+            const Q* e = reinterpret_cast<const Q*>(row) + (p.reverse ? H::TT - r.tl : 16 / (int)sizeof(Q) + r.tl - 4);
+            take_run<Q, 2>(e, false, h0);
+            take_run<Q, 2>(e + 2, false, h1);
+            xh[0] = p.reverse ? h1[0] : h0[1];
+            xh[1] = p.reverse ? h0[1] : h1[0];
+            xh[2] = p.reverse ? h0[0] : h1[1];
+            if constexpr (Q8) {
+                const float* sc = reinterpret_cast<const float*>(raw + R::SC);
+                const int pos0 = p.reverse ? L - t0 - H::TT : t0, blk0 = max(pos0 - 3, 0) / kBlock8;
 #pragma unroll
-            for (int m = 0; m < 3; ++m) {
-                const int o = r.tl - 3 + m;                    // scan offset within the tile
-                const int at = o >= 0 ? 16 / eq + (p.reverse ? H::TT - 1 - o : o)
-                                      : p.reverse ? -1 - o : 16 / eq + o;
-                if (t0 + o < 0) {
-                    xh[m] = past(r.ch, t0 + o);
-                } else if (Q8) {
-                    const int pos = p.reverse ? L - 1 - (t0 + o) : t0 + o;
-                    xh[m] = (float)reinterpret_cast<const int8_t*>(row)[at] *
-                            sc[(pos / kBlock8 == blk0 ? 0 : H::G) + r.ch];
-                } else {
-                    xh[m] = Elem<T>::to_f(reinterpret_cast<const T*>(row)[at]);
+                for (int m = 0; m < 3; ++m) {
+                    const int tm = t - 3 + m, pos = p.reverse ? L - 1 - tm : tm;
+                    xh[m] *= sc[(pos / kBlock8 == blk0 ? 0 : H::G) + r.ch];
                 }
             }
+            if (t < 3)                                         // before the row: its history
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    if (t - 3 + m < 0) xh[m] = past(r.ch, t - 3 + m);
             float w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = prm[r.ch * 8 + k];
+            auto tap = [&](int i, int lag) { return i >= lag ? u[i >= lag ? i - lag : 0] : xh[i >= lag ? 0 : 3 + i - lag]; };
+            if (!p.since) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int sn = p.since ? since[r.tl + i] : 4;
+                for (int i = 0; i < E; ++i)
 #pragma unroll
-                for (int lag = 0; lag < 4; ++lag) {
-                    const float v = i >= lag ? u[i >= lag ? i - lag : 0] : xh[i >= lag ? 0 : 3 + i - lag];
-                    if (lag <= sn) acc[i] = fmaf(w[3 - lag], v, acc[i]);
+                    for (int lag = 0; lag < 4; ++lag) acc[i] = fmaf(w[3 - lag], tap(i, lag), acc[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const int sn = since[r.tl + i];
+#pragma unroll
+                    for (int lag = 0; lag < 4; ++lag)
+                        if (lag <= sn) acc[i] = fmaf(w[3 - lag], tap(i, lag), acc[i]);
                 }
             }
         }
@@ -738,6 +810,8 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
     uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
     uint8_t* raw = reinterpret_cast<uint8_t*>(prm + H::kPrm + H::kMask);
     constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
+    using K = BwdCopies<T, S, CL, Q8, SUM>;
+    BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 2 * kRaw);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int j = lane % S, cl = lane / S;
     const int b = blockIdx.y, d0 = blockIdx.x * H::G, seg = blockIdx.z;
@@ -755,12 +829,14 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
         if (!SUM && seg == 0) load_state<S>(p, p.h0, b, d, j, h[kc]);
         if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc]);
     }
-    fetch_tile<T, S, CL, Q8, SUM>(p, b, d0, tb, raw);
+    if (p.async)                                               // a thread reads back its own entries
+        for (int k = tid; k < K::COUNT; k += kBwdThreads) table[k] = K::make(p, b, d0, k);
+    fetch_tile<T, S, CL, Q8, SUM>(p, table, b, d0, tb, raw);
     int buf = 0;
     for (int t0 = tb; t0 < te; t0 += H::TT, buf ^= 1) {
         cp_async_wait();
         __syncthreads();                                       // this tile is here, the last one used
-        if (t0 + H::TT < te) fetch_tile<T, S, CL, Q8, SUM>(p, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
+        if (t0 + H::TT < te) fetch_tile<T, S, CL, Q8, SUM>(p, table, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
         stage_tile<T, S, CL, Q8, SUM>(p, b, d0, t0, raw + buf * kRaw, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
         const uint32_t starts = *mask;
@@ -858,6 +934,8 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
     float* sums = carry + H::kCarry;
     uint8_t* raw = reinterpret_cast<uint8_t*>(sums + (CL ? H::kSum : 0));
     constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
+    using K = BwdCopies<T, S, CL, Q8, true>;
+    BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 2 * kRaw);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int j = lane % S, cl = lane / S;
     const int b = blockIdx.y, d0 = blockIdx.x * H::G, seg = blockIdx.z;
@@ -896,14 +974,16 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
     };
     uint64_t hn[2] = {0, 0};
     load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
-    fetch_tile<T, S, CL, Q8, true>(p, b, d0, tb + (ntiles - 1) * TT, raw);
+    if (p.async)                                               // a thread reads back its own entries
+        for (int k = tid; k < K::COUNT; k += kBwdThreads) table[k] = K::make(p, b, d0, k);
+    fetch_tile<T, S, CL, Q8, true>(p, table, b, d0, tb + (ntiles - 1) * TT, raw);
     int buf = 0;
     for (int tile = ntiles - 1; tile >= 0; --tile, buf ^= 1) {
         const int t0 = tb + tile * TT;
         const uint8_t* cur = raw + buf * kRaw;
         cp_async_wait();
         __syncthreads();                                       // this tile is here, the last one used
-        if (tile > 0) fetch_tile<T, S, CL, Q8, true>(p, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
+        if (tile > 0) fetch_tile<T, S, CL, Q8, true>(p, table, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
         stage_tile<T, S, CL, Q8, true>(p, b, d0, t0, cur, prm, st, gs, us, Bs, Cs, mask);
         __syncthreads();
         const uint32_t starts = *mask;
@@ -1025,7 +1105,7 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
         __syncthreads();
         // the tile's gradients, one run per thread
         {
-            const int d = d0 + run.ch, t = t0 + run.tl, dir = p.reverse ? -1 : 1;
+            const int d = d0 + run.ch, t = t0 + run.tl;
             const int pos = p.reverse ? L - 1 - t : t;
             const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
             if (hi > 0) {
@@ -1059,15 +1139,22 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                         dBias += ddt[i];
                     }
                 }
-                auto at = [&](const Str& s) {
-                    return (int64_t)b * s.b + (int64_t)d * s.c + (int64_t)pos * s.p;
-                };
-                auto step = [&](const Str& s) { return CL ? s.c : dir * s.p; };
-                if (p.du32) store_run<float, E>(p.du32 + at(p.sdu), step(p.sdu), 0, hi, du);
-                else store_run<T, E>(static_cast<T*>(p.du) + at(p.sdu), step(p.sdu), 0, hi, du);
-                store_run<T, E>(static_cast<T*>(p.ddt) + at(p.sddt), step(p.sddt), 0, hi, ddt);
-                if (p.z.p && p.dz)
-                    store_run<T, E>(static_cast<T*>(p.dz) + at(p.sdz), step(p.sdz), 0, hi, dz);
+                if constexpr (CL) {
+                    auto at = [&](const Str& s) { return (int64_t)b * s.b + d + (int64_t)pos * s.p; };
+                    if (p.du32) put_run<float, E>(p.du32 + at(p.sdu), false, p.vec_out, hi, du);
+                    else put_run<T, E>(static_cast<T*>(p.du) + at(p.sdu), false, p.vec_out, hi, du);
+                    put_run<T, E>(static_cast<T*>(p.ddt) + at(p.sddt), false, p.vec_out, hi, ddt);
+                    if (p.z.p && p.dz)
+                        put_run<T, E>(static_cast<T*>(p.dz) + at(p.sdz), false, p.vec_out, hi, dz);
+                } else {
+                    // dense rows: one offset for all, of the run's lowest position
+                    const bool rev = p.reverse;
+                    const int64_t at = ((int64_t)b * p.dim + d) * L + (rev ? pos - (E - 1) : pos);
+                    if (p.du32) put_run<float, E>(p.du32 + at, rev, p.vec_out, hi, du);
+                    else put_run<T, E>(static_cast<T*>(p.du) + at, rev, p.vec_out, hi, du);
+                    put_run<T, E>(static_cast<T*>(p.ddt) + at, rev, p.vec_out, hi, ddt);
+                    if (p.z.p && p.dz) put_run<T, E>(static_cast<T*>(p.dz) + at, rev, p.vec_out, hi, dz);
+                }
             }
         }
         // the CTA's dB and dC of the tile

@@ -24,13 +24,17 @@ inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t 
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid,
-                                (H::kSt + H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
+                                (H::kSt + H::kBC + H::kPrm + H::kMask) * 4 + kRaw + BwdCopies<T, S, CL, Q8, false>::COUNT * 16,
+                                p, st);
     if (what == 1)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kSummary>, grid,
-                                (H::kSt + H::kG + H::kU + 2 * H::kBC + H::kPrm + H::kMask) * 4 + kRaw, p, st);
+                                (H::kSt + H::kG + H::kU + 2 * H::kBC + H::kPrm + H::kMask) * 4 + kRaw +
+                                    BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
+                                p, st);
     return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid,
                             (H::kSt + H::kG + H::kU + 3 * H::kOut + 2 * H::kBC + H::kPart + H::kPrm +
-                             H::kMask + H::kCarry + (CL ? H::kSum : 0)) * 4 + kRaw,
+                             H::kMask + H::kCarry + (CL ? H::kSum : 0)) * 4 + kRaw +
+                                BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                             p, st);
 }
 

@@ -356,6 +356,9 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         c.part = f(pl.conv_part);
         c.chunks = pl.conv_chunks;
         c.chunk_len = conv_bwd_chunk(cl);
+        // runs of 8 positions, or channel-last of 4 channels (4 codes, 8 or 16 bytes)
+        c.vec = is_aligned(a->u, 16) && is_aligned(a->du, 16) &&
+                (cl ? (p.x.s.p % 4 == 0 && c.sdx.p % 4 == 0 && D % 4 == 0) : (L % 8 == 0 && !packed8));
         if ((e = launch_conv_bwd((int)es, cl, c, s)) != cudaSuccess)
             return api_cuda(e, "conv gradient launch");
         ConvReduceParams cr{(int)D, a->conv_width, Bn * pl.conv_chunks, c.part,
@@ -433,6 +436,7 @@ ssm_status_t ssm_causal_conv1d_bwd(const void* dout, const void* x, const float*
     c.part = static_cast<float*>(workspace);
     c.chunk_len = conv_bwd_chunk(false);
     c.chunks = (int)((seqlen + c.chunk_len - 1) / c.chunk_len);
+    c.vec = seqlen % 8 == 0 && is_aligned(x, 16) && is_aligned(dout, 16) && is_aligned(dx, 16);
     cudaError_t e = launch_conv_bwd((int)es, false, c, s);
     if (e != cudaSuccess) return api_cuda(e, "conv gradient launch");
     if (dw || dbias) {

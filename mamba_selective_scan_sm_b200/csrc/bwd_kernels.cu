@@ -26,19 +26,29 @@ __global__ void __launch_bounds__(256) since_kernel(const int32_t* cu, int nseq,
 // dB and dC: the sum over the channel groups of their partial rows, rounded once. A CTA
 // takes kReduceSteps steps of one batch row; the sums pass through shared memory, since
 // (batch, dstate, seqlen) outputs run along the steps and the partial rows along the states.
-constexpr int kReduceSteps = 16;
+constexpr int kReduceSteps = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bwd_reduce_bc_kernel(const BwdReduceParams p) {
+__global__ void __launch_bounds__(128) scan_bwd_reduce_bc_kernel(const BwdReduceParams p) {
     extern __shared__ float sm[];
     const int row = 2 * p.ns, b = blockIdx.y, t0 = blockIdx.x * kReduceSteps;
     const int nt = min(kReduceSteps, p.seqlen - t0);
     const int64_t gstride = (int64_t)p.batch * p.seqlen * row;
     const float* src = p.parts + ((int64_t)b * p.seqlen + t0) * row;
-    for (int k = threadIdx.x; k < nt * row; k += blockDim.x) {
-        float v = 0.f;
+    for (int k = threadIdx.x * 4; k < nt * row; k += blockDim.x * 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int g = 0; g < p.groups; ++g) v += src[g * gstride + k];
-        sm[(k / row) * (row + 1) + k % row] = v;
+        for (int g = 0; g < p.groups; ++g) {
+            const float4 q = *reinterpret_cast<const float4*>(src + g * gstride + k);
+            v.x += q.x;
+            v.y += q.y;
+            v.z += q.z;
+            v.w += q.w;
+        }
+        float* o = sm + (k / row) * (row + 1) + k % row;
+        o[0] = v.x;
+        o[1] = v.y;
+        o[2] = v.z;
+        o[3] = v.w;
     }
     __syncthreads();
     const bool along_p = p.sdB.p == 1 && p.sdB.c != 1;
@@ -79,12 +89,10 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_a_kernel(const BwdReduceP
 
 __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdReduceParams p) {
     const int h = blockIdx.x;
-    const int64_t per = (int64_t)p.head_dim * p.ns, first = h * per;
     float v = 0.f;
-    for (int r = 0; r < p.nrows; ++r) {
-        const float* src = p.pA + (int64_t)r * p.dim * p.ns + first;
-#pragma unroll 4
-        for (int64_t k = threadIdx.x; k < per; k += blockDim.x) v += src[k];
+    for (int r = 0; r < p.nrows; ++r) {                        // (nrows, dim): summed over the states
+        const float* src = p.pA + (int64_t)r * p.dim + (int64_t)h * p.head_dim;
+        for (int k = threadIdx.x; k < p.head_dim; k += blockDim.x) v += src[k];
     }
     __shared__ float red[256 / 32];
 #pragma unroll
@@ -121,8 +129,8 @@ cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st) {
 cudaError_t launch_scan_bwd_reduce(int elem_size, const BwdReduceParams& p, cudaStream_t st) {
     const dim3 g((p.seqlen + kReduceSteps - 1) / kReduceSteps, p.batch);
     const int smem = kReduceSteps * (2 * p.ns + 1) * (int)sizeof(float);
-    if (elem_size == 2) scan_bwd_reduce_bc_kernel<__nv_bfloat16><<<g, 256, smem, st>>>(p);
-    else scan_bwd_reduce_bc_kernel<float><<<g, 256, smem, st>>>(p);
+    if (elem_size == 2) scan_bwd_reduce_bc_kernel<__nv_bfloat16><<<g, 128, smem, st>>>(p);
+    else scan_bwd_reduce_bc_kernel<float><<<g, 128, smem, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t n = (p.head_dim ? 0 : (int64_t)p.dim * p.ns) + 2 * (int64_t)p.dim;
@@ -144,8 +152,14 @@ cudaError_t launch_conv_bwd(int elem_size, bool channel_last, const ConvBwdParam
     if (channel_last) {
         const int per = 128 * kConvClRun;
         const dim3 g((p.dim + per - 1) / per, p.batch, p.chunks);
-        if (elem_size == 2) conv_bwd_cl_kernel<__nv_bfloat16><<<g, 128, 0, st>>>(p);
-        else conv_bwd_cl_kernel<float><<<g, 128, 0, st>>>(p);
+        const bool q8 = p.x.scale != nullptr;
+        if (elem_size == 2) {
+            if (q8) conv_bwd_cl_kernel<__nv_bfloat16, true><<<g, 128, 0, st>>>(p);
+            else conv_bwd_cl_kernel<__nv_bfloat16, false><<<g, 128, 0, st>>>(p);
+        } else {
+            if (q8) conv_bwd_cl_kernel<float, true><<<g, 128, 0, st>>>(p);
+            else conv_bwd_cl_kernel<float, false><<<g, 128, 0, st>>>(p);
+        }
     } else {
         const int64_t rows = (int64_t)p.batch * p.dim;
         const dim3 g(p.chunks, (unsigned)(rows < 65535 ? rows : 65535), (unsigned)((rows + 65534) / 65535));
@@ -156,7 +170,7 @@ cudaError_t launch_conv_bwd(int elem_size, bool channel_last, const ConvBwdParam
 }
 
 cudaError_t launch_conv_reduce(const ConvReduceParams& p, cudaStream_t st) {
-    conv_reduce_kernel<<<(unsigned)(((int64_t)p.dim * 5 + 127) / 128), 128, 0, st>>>(p);
+    conv_reduce_kernel<<<(unsigned)(((int64_t)p.dim * 5 + 31) / 32), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -45,7 +45,7 @@ struct BwdParams {
     float* ckpt;                  // states before every kSubSteps-th step
     int nsub;                     // checkpoints per row: ceil(seqlen / tile) * tile / kSubSteps
     float* parts;                 // (groups, batch, seqlen, 2, NS): dB, dC of a channel group
-    float* pA;                    // (nseg * batch, dim, NS)
+    float* pA;                    // (nseg * batch, dim, NS); with A per head (nseg * batch, dim)
     float* pD;                    // (nseg * batch, dim, 2): dD, d delta_bias
     float *sumP, *sumS, *sumR;    // (nseg, batch, dim, NS) segment summaries, then carries
     int nseg, seg_len;
@@ -60,6 +60,7 @@ struct ConvBwdParams {
     Str sdo;
     const float *w, *bias;
     int silu, reverse;
+    int vec;                      // runs of x, dout and dx are aligned to their size, rows whole runs
     const void* hist;
     const uint8_t* since;
     void* dx;

@@ -18,6 +18,7 @@ constexpr int kConvRowThreads = 128;
 constexpr int kConvRowChunk = kConvRun * kConvRowThreads;      // steps per CTA along a row
 constexpr int kConvClChunk = 64;                               // steps per thread, channel-last
 constexpr int kConvClRun = 4;                                  // channels per thread
+constexpr int kConvClAhead = 4;                                // steps whose loads are issued together
 
 // d silu(v) / dv
 __device__ __forceinline__ float dsilu(float v) {
@@ -32,6 +33,12 @@ __device__ __forceinline__ float conv_hist(const ConvBwdParams& p, int b, int d,
                ? Elem<T>::to_f(static_cast<const T*>(
                      p.hist)[((int64_t)b * p.dim + d) * (p.width - 1) + (p.width - 1 + t)])
                : 0.f;
+}
+
+// R elements from p on in the run's direction (rev: towards lower positions), aligned.
+template <typename T, int R>
+__device__ __forceinline__ void take_dense(const T* p, bool rev, float (&f)[R]) {
+    take_run<T, R>(rev ? p - (R - 1) : p, rev, f);
 }
 
 template <typename T>
@@ -50,56 +57,92 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
     float sw[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
     if (t0 < L) {
         // x[t0 - 3 .. t0 + 10], dpre[t0 .. t0 + 10]
-        float x[R + 6], dp[R + 3], run[R];
-        auto pos = [&](int t) { return p.reverse ? L - 1 - t : t; };
-        load_act<T, R>(p.x, b, d, pos(t0), dir, true, 0, L - t0, run);
+        float x[R + 6], dp[R + 3];
+        const bool rev = p.reverse;
+        const int pos0 = rev ? L - 1 - t0 : t0;
+        const T* xr = static_cast<const T*>(p.x.p) + (int64_t)b * p.x.s.b + (int64_t)d * p.x.s.c;
+        const int64_t orow = (int64_t)b * p.sdo.b + (int64_t)d * p.sdo.c;
+        if (p.vec) {
+            // whole rows of aligned runs: the run, 4 steps behind it and 4 before it
+            float run[R], near[4];
+            take_dense<T, R>(xr + pos0, rev, run);
 #pragma unroll
-        for (int i = 0; i < R; ++i) x[3 + i] = run[i];
+            for (int i = 0; i < R; ++i) x[3 + i] = run[i];
+            if (t0 > 0) {
+                take_dense<T, 4>(xr + pos0 - dir * 4, rev, near);
 #pragma unroll
-        for (int m = 0; m < 6; ++m) {
-            const int i = m < 3 ? m : R + m, t = t0 - 3 + i;
-            float one[1] = {0.f};
-            if (t >= 0) load_act<T, 1>(p.x, b, d, pos(t), dir, true, 0, t < L ? 1 : 0, one);
-            else one[0] = conv_hist<T>(p, b, d, t);
-            x[i] = one[0];
-        }
-        const int64_t o = (int64_t)b * p.sdo.b + (int64_t)d * p.sdo.c + (int64_t)pos(t0) * p.sdo.p;
-        const int64_t os = dir * p.sdo.p;
-        if (p.dout32) load_run<float, R>(static_cast<const float*>(p.dout) + o, os, 0, L - t0, run);
-        else load_run<T, R>(static_cast<const T*>(p.dout) + o, os, 0, L - t0, run);
+                for (int i = 0; i < 3; ++i) x[i] = near[i + 1];
+            } else {
 #pragma unroll
-        for (int i = 0; i < R + 3; ++i) {
-            if (i < R) dp[i] = run[i < R ? i : 0];
-            else if (t0 + i >= L) dp[i] = 0.f;
-            else dp[i] = p.dout32 ? static_cast<const float*>(p.dout)[o + i * os]
-                                  : Elem<T>::to_f(static_cast<const T*>(p.dout)[o + i * os]);
+                for (int i = 0; i < 3; ++i) x[i] = conv_hist<T>(p, b, d, i - 3);
+            }
+            const bool more = t0 + R < L;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) near[i] = 0.f;
+            if (more) take_dense<T, 4>(xr + pos0 + dir * R, rev, near);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) x[R + 3 + i] = near[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) near[i] = 0.f;
+            if (p.dout32) {
+                const float* o = static_cast<const float*>(p.dout) + orow + pos0;
+                take_dense<float, R>(o, rev, run);
+                if (more) take_dense<float, 4>(o + dir * R, rev, near);
+            } else {
+                const T* o = static_cast<const T*>(p.dout) + orow + pos0;
+                take_dense<T, R>(o, rev, run);
+                if (more) take_dense<T, 4>(o + dir * R, rev, near);
+            }
+#pragma unroll
+            for (int i = 0; i < R + 3; ++i) dp[i] = i < R ? run[i < R ? i : 0] : near[i < R ? 0 : i - R];
+        } else {
+#pragma unroll
+            for (int i = 0; i < R + 6; ++i) {
+                const int t = t0 - 3 + i;
+                float one[1] = {0.f};
+                if (t < 0) one[0] = conv_hist<T>(p, b, d, t);
+                else if (t < L) load_act<T, 1>(p.x, b, d, rev ? L - 1 - t : t, dir, true, 0, 1, one);
+                x[i] = one[0];
+            }
+#pragma unroll
+            for (int i = 0; i < R + 3; ++i) {
+                const int64_t o = orow + (int64_t)(pos0 + dir * i) * p.sdo.p;
+                dp[i] = t0 + i >= L ? 0.f
+                        : p.dout32  ? static_cast<const float*>(p.dout)[o]
+                                    : Elem<T>::to_f(static_cast<const T*>(p.dout)[o]);
+            }
         }
         float dx[R + 3];                                       // dx[t0 - 3 .. t0 + 7]
 #pragma unroll
         for (int i = 0; i < R + 3; ++i) dx[i] = 0.f;
+        auto steps = [&](auto packed) {
 #pragma unroll
-        for (int i = 0; i < R + 3; ++i) {
-            const int sn = p.since && t0 + i < L ? p.since[t0 + i] : 4;
-            if (p.silu) {
-                float pre = bias;
+            for (int i = 0; i < R + 3; ++i) {
+                const int sn = decltype(packed)::value && t0 + i < L ? p.since[t0 + i] : 4;
+                if (p.silu) {
+                    float pre = bias;
+#pragma unroll
+                    for (int lag = 0; lag < 4; ++lag)
+                        if (lag <= sn) pre = fmaf(w[lag], x[3 + i - lag], pre);
+                    dp[i] *= dsilu(pre);
+                }
 #pragma unroll
                 for (int lag = 0; lag < 4; ++lag)
-                    if (lag <= sn) pre = fmaf(w[lag], x[3 + i - lag], pre);
-                dp[i] *= dsilu(pre);
+                    if (lag <= sn) {
+                        if (i - lag < R)
+                            dx[i - lag < R ? 3 + i - lag : 0] = fmaf(w[lag], dp[i], dx[i - lag < R ? 3 + i - lag : 0]);
+                        if (i < R) sw[lag] = fmaf(dp[i], x[3 + i - lag], sw[lag]);
+                    }
+                if (i < R) sw[4] += dp[i];
             }
+        };
+        if (p.since) steps(std::true_type{});
+        else steps(std::false_type{});
+        float out[R];
 #pragma unroll
-            for (int lag = 0; lag < 4; ++lag)
-                if (lag <= sn) {
-                    if (i - lag < R) dx[3 + i - lag < R + 3 ? 3 + i - lag : 0] += w[lag] * dp[i];
-                    if (i < R) sw[lag] = fmaf(dp[i], x[3 + i - lag], sw[lag]);
-                }
-            if (i < R) sw[4] += dp[i];
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) run[i] = dx[3 + i];
-        store_run<T, R>(static_cast<T*>(p.dx) + (int64_t)b * p.sdx.b + (int64_t)d * p.sdx.c +
-                            (int64_t)pos(t0) * p.sdx.p,
-                        dir * p.sdx.p, 0, L - t0, run);
+        for (int i = 0; i < R; ++i) out[i] = dx[3 + i];
+        T* o = static_cast<T*>(p.dx) + (int64_t)b * p.sdx.b + (int64_t)d * p.sdx.c + pos0;
+        put_run<T, R>(rev ? o - (R - 1) : o, rev, p.vec, min(R, L - t0), out);
         if (t0 == 0 && p.dhist)
 #pragma unroll
             for (int m = 0; m < 3; ++m)                        // positions -3 .. -1
@@ -123,10 +166,30 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
     }
 }
 
-template <typename T>
+// E values of x or dout at a step, as they come: VEC in one load where p.vec says that whole
+// runs are aligned to their size (a bf16 run of 4 in 8 bytes, fp32 in 16), else by element.
+template <typename Q, int E>
+__device__ __forceinline__ void take_or(const Q* p, bool vec, int hi, float (&f)[E]) {
+    if (vec && hi == E) {
+        take_run<Q, E>(p, false, f);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        f[i] = 0.f;
+        if (i < hi) {
+            if constexpr (sizeof(Q) == 1) f[i] = (float)p[i];
+            else f[i] = Elem<Q>::to_f(p[i]);
+        }
+    }
+}
+
+// Channel-last: only the scan's gradient calls it, with dout in fp32 (dout32).
+template <typename T, bool Q8>
 __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p) {
-    constexpr int E = kConvClRun;
-    const int L = p.seqlen, dir = p.reverse ? -1 : 1;
+    constexpr int E = kConvClRun, U = kConvClAhead;
+    using X = std::conditional_t<Q8, int8_t, T>;
+    const int L = p.seqlen;
     const int d = (blockIdx.x * blockDim.x + threadIdx.x) * E;
     const int b = blockIdx.y, chunk = blockIdx.z;
     if (d >= p.dim) return;
@@ -145,64 +208,82 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
         xw[3][i] = 0.f;
     }
     auto pos = [&](int t) { return p.reverse ? L - 1 - t : t; };
-    auto load_x = [&](int t, float (&v)[E]) {
-        if (t >= 0) {
-            load_act<T, E>(p.x, b, d, pos(t), dir, false, 0, t < L ? hi : 0, v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = i < hi ? conv_hist<T>(p, b, d + i, t) : 0.f;
-        }
-    };
-    // xw[lag] holds x_{t-lag}; before the first step x_{tb-1-lag}
-#pragma unroll
-    for (int lag = 0; lag < 3; ++lag) load_x(tb - 1 - lag, xw[lag]);
-#pragma unroll 4
-    for (int t = tb; t < te + 3; ++t) {
-        float x[E], dp[E];
-        load_x(t, x);
-        const int64_t o = (int64_t)b * p.sdo.b + (int64_t)d * p.sdo.c + (int64_t)pos(t) * p.sdo.p;
-        const int h = t < L ? hi : 0;
-        if (p.dout32) load_run<float, E>(static_cast<const float*>(p.dout) + o, p.sdo.c, 0, h, dp);
-        else load_run<T, E>(static_cast<const T*>(p.dout) + o, p.sdo.c, 0, h, dp);
-        const int sn = p.since && t < L ? p.since[t] : 4;
-        float out[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            xw[3][i] = xw[2][i];
-            xw[2][i] = xw[1][i];
-            xw[1][i] = xw[0][i];
-            xw[0][i] = x[i];
-            acc[3][i] = acc[2][i];                             // acc[lag]: dx_{t-lag} so far
-            acc[2][i] = acc[1][i];
-            acc[1][i] = acc[0][i];
-            acc[0][i] = 0.f;
-            if (p.silu) {
-                float pre = bias[i];
-#pragma unroll
-                for (int lag = 0; lag < 4; ++lag)
-                    if (lag <= sn) pre = fmaf(w[lag][i], xw[lag][i], pre);
-                dp[i] *= dsilu(pre);
-            }
-#pragma unroll
-            for (int lag = 0; lag < 4; ++lag)
-                if (lag <= sn) {
-                    acc[lag][i] = fmaf(w[lag][i], dp[i], acc[lag][i]);
-                    if (t < te) sw[lag][i] = fmaf(dp[i], xw[lag][i], sw[lag][i]);
-                }
-            if (t < te) sw[4][i] += dp[i];
-            out[i] = acc[3][i];
-        }
-        const int s = t - 3;                                   // dx_s is complete
-        if (s >= tb) {
-            store_run<T, E>(static_cast<T*>(p.dx) + (int64_t)b * p.sdx.b + (int64_t)d * p.sdx.c +
-                                (int64_t)pos(s) * p.sdx.p,
-                            p.sdx.c, 0, hi, out);
-        } else if (chunk == 0 && p.dhist && s >= -(p.width - 1)) {
+    const X* xb = static_cast<const X*>(p.x.p) + (int64_t)b * p.x.s.b + d;
+    const float* yb = static_cast<const float*>(p.dout) + (int64_t)b * p.sdo.b + d;
+    auto scaled = [&](int t, float (&v)[E]) {                  // codes to values
+        if constexpr (Q8)
 #pragma unroll
             for (int i = 0; i < E; ++i)
                 if (i < hi)
-                    static_cast<T*>(p.dhist)[((int64_t)b * p.dim + d + i) * (p.width - 1) +
-                                             (p.width - 1 + s)] = Elem<T>::from_f(out[i]);
+                    v[i] *= p.x.scale[(int64_t)b * p.x.ss.b + (int64_t)(pos(t) / kBlock8) * p.x.ss.p + d + i];
+    };
+    // xw[lag] holds x_{t-lag}; before the first step x_{tb-1-lag}
+#pragma unroll
+    for (int lag = 0; lag < 3; ++lag) {
+        const int t = tb - 1 - lag;
+        if (t >= 0) {
+            take_or<X, E>(xb + (int64_t)pos(t) * p.x.s.p, p.vec, hi, xw[lag]);
+            scaled(t, xw[lag]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) xw[lag][i] = i < hi ? conv_hist<T>(p, b, d + i, t) : 0.f;
+        }
+    }
+    for (int tu = tb; tu < te + 3; tu += U) {
+        float x[U][E], dp[U][E];
+        int sn[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {                          // every load before the first use
+            const int t = tu + k, n = t < L && t < te + 3 ? hi : 0;
+            const int64_t ps = n ? pos(t) : 0;
+            take_or<X, E>(xb + ps * p.x.s.p, p.vec, n, x[k]);
+            take_or<float, E>(yb + ps * p.sdo.p, p.vec, n, dp[k]);
+            sn[k] = p.since && n ? p.since[t] : 4;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int t = tu + k;
+            if (t >= te + 3) break;
+            if (t < L) scaled(t, x[k]);
+            float out[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                xw[3][i] = xw[2][i];
+                xw[2][i] = xw[1][i];
+                xw[1][i] = xw[0][i];
+                xw[0][i] = x[k][i];
+                acc[3][i] = acc[2][i];                         // acc[lag]: dx_{t-lag} so far
+                acc[2][i] = acc[1][i];
+                acc[1][i] = acc[0][i];
+                acc[0][i] = 0.f;
+                float g = dp[k][i];
+                if (p.silu) {
+                    float pre = bias[i];
+#pragma unroll
+                    for (int lag = 0; lag < 4; ++lag)
+                        if (lag <= sn[k]) pre = fmaf(w[lag][i], xw[lag][i], pre);
+                    g *= dsilu(pre);
+                }
+#pragma unroll
+                for (int lag = 0; lag < 4; ++lag)
+                    if (lag <= sn[k]) {
+                        acc[lag][i] = fmaf(w[lag][i], g, acc[lag][i]);
+                        if (t < te) sw[lag][i] = fmaf(g, xw[lag][i], sw[lag][i]);
+                    }
+                if (t < te) sw[4][i] += g;
+                out[i] = acc[3][i];
+            }
+            const int s = t - 3;                               // dx_s is complete
+            if (s >= tb) {
+                put_run<T, E>(static_cast<T*>(p.dx) + (int64_t)b * p.sdx.b + d + (int64_t)pos(s) * p.sdx.p,
+                              false, p.vec, hi, out);
+            } else if (chunk == 0 && p.dhist && s >= -(p.width - 1)) {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    if (i < hi)
+                        static_cast<T*>(p.dhist)[((int64_t)b * p.dim + d + i) * (p.width - 1) +
+                                                 (p.width - 1 + s)] = Elem<T>::from_f(out[i]);
+            }
         }
     }
 #pragma unroll
@@ -213,14 +294,23 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
                 p.part[(((int64_t)b * p.chunks + chunk) * p.dim + d + i) * 5 + k] = sw[k][i];
 }
 
-// dw (dim, width), dbias (dim) from the partial rows (rows, dim, 5: by lag, then bias).
-__global__ void __launch_bounds__(128) conv_reduce_kernel(const ConvReduceParams p) {
-    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (idx >= (int64_t)p.dim * 5) return;
-    const int d = (int)(idx / 5), k = (int)(idx % 5);
+// dw (dim, width), dbias (dim) from the partial rows (rows, dim, 5: by lag, then bias). A CTA
+// takes 32 columns; its 8 warps take the rows in turn and meet in shared memory.
+__global__ void __launch_bounds__(256) conv_reduce_kernel(const ConvReduceParams p) {
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t idx = (int64_t)blockIdx.x * 32 + lane;
     float v = 0.f;
+    if (idx < (int64_t)p.dim * 5) {
 #pragma unroll 8
-    for (int64_t r = 0; r < p.rows; ++r) v += p.part[r * p.dim * 5 + idx];
+        for (int64_t r = warp; r < p.rows; r += 8) v += p.part[r * p.dim * 5 + idx];
+    }
+    red[warp][lane] = v;
+    __syncthreads();
+    if (warp != 0 || idx >= (int64_t)p.dim * 5) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += red[k][lane];
+    const int d = (int)(idx / 5), k = (int)(idx % 5);
     if (k < 4) {
         if (p.dw && k < p.width) p.dw[(int64_t)d * p.width + p.width - 1 - k] = v;
     } else if (p.dbias) {

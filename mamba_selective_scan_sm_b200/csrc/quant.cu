@@ -2,6 +2,8 @@
 #define SSM_ERROR_WORD g_error_quant
 #include "quant_kernel.cuh"
 
+#include <type_traits>
+
 #include "api_common.h"
 
 namespace ssm {
@@ -34,44 +36,72 @@ cudaError_t launch_unpack(int elem_size, bool channel_last, const PackParams& p,
 }
 
 namespace {
-int lanes_per_row(int dstate) {
-    int l = 1;
-    while (16 * l < dstate) l *= 2;
-    return l;
+// K<LPR> for rows of NP states a lane
+template <int NP, typename F>
+void by_lanes(int dstate, F&& f) {
+    if (dstate <= NP) f(std::integral_constant<int, 1>{});
+    else if (dstate <= 2 * NP) f(std::integral_constant<int, 2>{});
+    else if (dstate <= 4 * NP) f(std::integral_constant<int, 4>{});
+    else if (dstate <= 8 * NP) f(std::integral_constant<int, 8>{});
+    else f(std::integral_constant<int, 16>{});
 }
-// 16-byte accesses of a lane's 16 codes
-bool vec_codes(const CacheParams& p) { return p.dstate % 16 == 0 && is_aligned(p.codes, 16); }
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
 }  // namespace
 
-// K<LPR, VEC> for the row's lanes and the codes' alignment
-#define SSM_CACHE(K_, ...)                                                                    \
-    do {                                                                                      \
-        const int l = lanes_per_row(p.dstate);                                                \
-        const unsigned g = (unsigned)((p.batch * p.dim * l + 255) / 256);                     \
-        const bool v = vec_codes(p);                                                          \
-        if (l == 1) v ? K_<__VA_ARGS__ 1, true><<<g, 256, 0, st>>>(p) : K_<__VA_ARGS__ 1, false><<<g, 256, 0, st>>>(p); \
-        if (l == 2) v ? K_<__VA_ARGS__ 2, true><<<g, 256, 0, st>>>(p) : K_<__VA_ARGS__ 2, false><<<g, 256, 0, st>>>(p); \
-        if (l == 4) v ? K_<__VA_ARGS__ 4, true><<<g, 256, 0, st>>>(p) : K_<__VA_ARGS__ 4, false><<<g, 256, 0, st>>>(p); \
-        if (l == 8) v ? K_<__VA_ARGS__ 8, true><<<g, 256, 0, st>>>(p) : K_<__VA_ARGS__ 8, false><<<g, 256, 0, st>>>(p); \
-    } while (0)
-#define SSM_COMMA ,
-
 cudaError_t launch_cache_write(const CacheParams& p, cudaStream_t st) {
-    SSM_CACHE(cache_write_kernel, );
+    by_lanes<8>(p.dstate, [&](auto l) {
+        constexpr int L = decltype(l)::value;
+        const int64_t per = 256 / L * kCacheRows;
+        cache_write_kernel<L><<<(unsigned)((p.batch * p.dim + per - 1) / per), 256, 0, st>>>(p);
+    });
     return cudaGetLastError();
 }
+
 cudaError_t launch_cache_read(int elem_size, const CacheParams& p, cudaStream_t st) {
-    if (elem_size == 2) SSM_CACHE(cache_read_kernel, __nv_bfloat16 SSM_COMMA);
-    else SSM_CACHE(cache_read_kernel, float SSM_COMMA);
+    by_lanes<8>(p.dstate, [&](auto l) {
+        constexpr int L = decltype(l)::value;
+        const unsigned g = blocks_of(p.batch * p.dim * L);
+        if (elem_size == 2) cache_read_kernel<__nv_bfloat16, L><<<g, 256, 0, st>>>(p);
+        else cache_read_kernel<float, L><<<g, 256, 0, st>>>(p);
+    });
     return cudaGetLastError();
 }
-cudaError_t launch_cached_update(int elem_size, const CacheParams& p, cudaStream_t st) {
-    if (elem_size == 2) SSM_CACHE(cached_update_kernel, __nv_bfloat16 SSM_COMMA);
-    else SSM_CACHE(cached_update_kernel, float SSM_COMMA);
-    return cudaGetLastError();
+
+cudaError_t launch_cached_update(int elem_size, CacheParams p, cudaStream_t st) {
+    cudaError_t e = cudaErrorInvalidValue;
+    by_lanes<16>(p.dstate, [&](auto l) {
+        constexpr int L = decltype(l)::value <= 8 ? decltype(l)::value : 8;
+        const int64_t gx = (p.dim + kUpdateThreads / L - 1) / (kUpdateThreads / L);
+        // the fewest batch rows a CTA with which all CTAs are resident at once (a second, part
+        // wave costs as much as a full one), up to what its shared memory holds
+        const int64_t slots = 148 * kUpdateCtas;
+        int64_t rows = 1;
+        while (rows < update_rows(L) && gx * ((p.batch + rows - 1) / rows) > slots) ++rows;
+        p.rows_per_cta = (int)rows;
+        // one launch, but for batches of more than 65535 CTAs
+        for (int64_t b = 0; b < p.batch; b += 65535ll * p.rows_per_cta) {
+            p.first_row = b;
+            const int64_t left = (p.batch - b + p.rows_per_cta - 1) / p.rows_per_cta;
+            const dim3 g((unsigned)gx, (unsigned)(left < 65535 ? left : 65535));
+            auto go = [&](auto elem, auto async, auto heads) {
+                cached_update_kernel<decltype(elem), L, decltype(async)::value, decltype(heads)::value>
+                    <<<g, kUpdateThreads, 0, st>>>(p);
+            };
+            auto pick = [&](auto elem) {
+                std::true_type yes;
+                std::false_type no;
+                if (p.async && p.head_dim) go(elem, yes, yes);
+                else if (p.async) go(elem, yes, no);
+                else if (p.head_dim) go(elem, no, yes);
+                else go(elem, no, no);
+            };
+            if (elem_size == 2) pick(__nv_bfloat16{});
+            else pick(float{});
+            if ((e = cudaGetLastError()) != cudaSuccess) return;
+        }
+    });
+    return e;
 }
-#undef SSM_CACHE
-#undef SSM_COMMA
 
 }  // namespace ssm
 
@@ -104,10 +134,10 @@ ssm_status_t check_cache(int64_t batch, int64_t dim, int64_t dstate, int64_t num
                         SSM_MAX_SCAN_DSTATE);
     if (dim > 0x3fffffffLL || batch > 0x3fffffffLL || num_slots > 0x7fffffffLL)
         return api_fail(SSM_ERR_BAD_SHAPE, "batch and dim must be below 2^30, num_slots below 2^31");
-    if (batch * dim > (int64_t)1 << 32)
-        return api_fail(SSM_ERR_BAD_SHAPE, "batch * dim exceeds 2^32");
-    if ((double)num_slots * dim * dstate > 1.1e12)
-        return api_fail(SSM_ERR_BAD_SHAPE, "the cache exceeds 2^40 bytes");
+    if (batch * dim > 0x7fffffffLL)
+        return api_fail(SSM_ERR_BAD_SHAPE, "batch * dim must be below 2^31");
+    if (num_slots > 0 && dim > 0xffffffffLL / num_slots)
+        return api_fail(SSM_ERR_BAD_SHAPE, "num_slots * dim must be below 2^32");
     if (!slots && num_slots < batch)
         return api_fail(SSM_ERR_BAD_SHAPE, "num_slots %lld < batch %lld without slots",
                         (long long)num_slots, (long long)batch);
@@ -291,6 +321,8 @@ ssm_status_t ssm_selective_state_update_cached(const ssm_cached_update_args_t* a
     p.conv_width = a->conv_weight ? a->conv_width : 0;
     p.softplus = a->dt_softplus ? 1 : 0;
     p.head_dim = a->a_heads > 0 ? (int)(a->dim / a->a_heads) : 0;
+    p.async = a->dstate % 16 == 0 && is_aligned(a->codes, 16) &&
+              (!a->conv_weight || (a->conv_width == 4 && is_aligned(a->conv_state, 4 * es)));
     cudaError_t e = launch_cached_update((int)es, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? api_ok() : api_cuda(e, "cached state update launch");
 }

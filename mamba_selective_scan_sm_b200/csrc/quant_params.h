@@ -29,12 +29,15 @@ struct CacheParams {
     const void *x, *dt, *Bt, *Ct, *z;
     const float *A, *D, *dt_bias, *conv_w, *conv_b;
     int conv_width, softplus, head_dim;
+    int async;                    // 16-byte aligned codes of 16 states; conv_width 4, aligned, or none
+    int rows_per_cta;             // batch rows of a CTA
+    int64_t first_row;            // of the launch
 };
 
 cudaError_t launch_pack(int elem_size, bool channel_last, const PackParams& p, cudaStream_t st);
 cudaError_t launch_unpack(int elem_size, bool channel_last, const PackParams& p, cudaStream_t st);
 cudaError_t launch_cache_write(const CacheParams& p, cudaStream_t st);
 cudaError_t launch_cache_read(int elem_size, const CacheParams& p, cudaStream_t st);
-cudaError_t launch_cached_update(int elem_size, const CacheParams& p, cudaStream_t st);
+cudaError_t launch_cached_update(int elem_size, CacheParams p, cudaStream_t st);
 
 }  // namespace ssm

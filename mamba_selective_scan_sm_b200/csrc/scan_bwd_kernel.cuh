@@ -1187,8 +1187,15 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
             ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
             ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
         }
+        if constexpr (HEADS) {                                 // (rows, dim): summed over the states
+            const float2 f = upk2(add2(dA[r][0], dA[r][1]));
+            float v = f.x + f.y;
+#pragma unroll
+            for (int w = 1; w < S; w *= 2) v += __shfl_xor_sync(0xffffffffu, v, w);
+            if (j == 0 && d < p.dim) p.pA[row * p.dim + d] = v;
+        }
         if (d < p.dim) {
-            stpair(p.pA + ns_off<S>(p, row, d, j), dA[r]);
+            if constexpr (!HEADS) stpair(p.pA + ns_off<S>(p, row, d, j), dA[r]);
             if (seg == 0 && p.dh0) {
                 const float2 lo = upk2(m[r][0]), hi = upk2(m[r][1]);
                 const float f[4] = {lo.x, lo.y, hi.x, hi.y};

@@ -96,7 +96,7 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     const int64_t per = (ntiles + nseg - 1) / nseg;
     pl->seg_len = (int)std::min<int64_t>(per * tile, 0x40000000);
     pl->nseg = (int)((ntiles + per - 1) / per);
-    pl->nsub = (int)(ntiles * tile / kSubSteps);
+    pl->nsub = (int)(ntiles * tile / pl->v.steps);
     const int chunk = conv_bwd_chunk(a->channel_last != 0);
     pl->conv_chunks = (int)((L + chunk - 1) / chunk);
 
@@ -320,6 +320,7 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     r.nrows = (int)(pl.nseg * Bn);
     r.reverse = p.reverse;
     r.head_dim = p.head_dim;
+    r.order_shift = pl.v.order_shift;
     r.order_mask = pl.v.order_mask;
     r.parts = p.parts;
     r.pA = p.pA;

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_a_kernel(const BwdReduceP
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t na = p.head_dim ? 0 : (int64_t)p.dim * p.ns;
     if (idx < na) {
-        const int d = (int)(idx / p.ns), n = (int)(idx % p.ns) ^ (d & p.order_mask);
+        const int d = (int)(idx / p.ns), n = (int)(idx % p.ns) ^ (d >> p.order_shift & p.order_mask);
         if (n >= p.dstate) return;
         float v = 0.f;
 #pragma unroll 8
@@ -106,11 +106,17 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdRed
     }
 }
 
+template <int S> static BwdVariant variant_of() {
+    using H = BwdShape<S>;
+    return {H::NS, H::G, H::TT, H::T, H::KL - 1, H::NC - 1};
+}
 BwdVariant scan_bwd_variant(int lanes) {
-#define SSM_BWD(S_) if (lanes == S_) return {BwdShape<S_>::NS, BwdShape<S_>::G, BwdShape<S_>::TT, BwdShape<S_>::NC - 1};
-    SSM_BWD(1) SSM_BWD(2) SSM_BWD(4) SSM_BWD(8) SSM_BWD(16)
-#undef SSM_BWD
-    return {BwdShape<32>::NS, BwdShape<32>::G, BwdShape<32>::TT, BwdShape<32>::NC - 1};
+    return lanes == 1   ? variant_of<1>()
+           : lanes == 2 ? variant_of<2>()
+           : lanes == 4 ? variant_of<4>()
+           : lanes == 8 ? variant_of<8>()
+           : lanes == 16 ? variant_of<16>()
+                         : variant_of<32>();
 }
 
 cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st) {

@@ -10,7 +10,8 @@ namespace ssm {
 // Static shape of the backward scan kernels for `lanes` (1, 2, .. 32) lanes per channel.
 struct BwdVariant {
     int ns, channels, tile;
-    int order_mask;               // scratch states of channel d stand at n ^ (d & order_mask)
+    int steps;                    // between two checkpoints of the state
+    int order_shift, order_mask;  // scratch states of channel d stand at n ^ (d >> shift & mask)
 };
 BwdVariant scan_bwd_variant(int lanes);
 

@@ -21,7 +21,6 @@ struct ActIn {
 };
 
 constexpr int kBlock8 = 64;       // positions per scale of an 8-bit activation
-constexpr int kSubSteps = 8;      // steps whose states the backward sweep holds in registers
 
 struct BwdParams {
     int batch, dim, seqlen, dstate;
@@ -42,8 +41,8 @@ struct BwdParams {
     void *ddt, *dz;
     Str sdu, sddt, sdz;
     float* dh0;                   // (batch, dim, dstate) or null
-    float* ckpt;                  // states before every kSubSteps-th step
-    int nsub;                     // checkpoints per row: ceil(seqlen / tile) * tile / kSubSteps
+    float* ckpt;                  // states before every BwdShape::T-th step
+    int nsub;                     // checkpoints per row, of whole tiles
     float* parts;                 // (groups, batch, seqlen, 2, NS): dB, dC of a channel group
     float* pA;                    // (nseg * batch, dim, NS); with A per head (nseg * batch, dim)
     float* pD;                    // (nseg * batch, dim, 2): dD, d delta_bias
@@ -72,7 +71,7 @@ struct ConvBwdParams {
 
 // Sums the partial results of a backward pass.
 struct BwdReduceParams {
-    int batch, dim, seqlen, dstate, ns, groups, nrows, reverse, head_dim, order_mask;
+    int batch, dim, seqlen, dstate, ns, groups, nrows, reverse, head_dim, order_shift, order_mask;
     const float *parts, *pA, *pD;
     void *dB, *dC;                // in the activations' type
     Str sdB, sdC;

@@ -36,8 +36,6 @@
 
 namespace ssm {
 
-constexpr int kBwdWarps = 4;
-constexpr int kBwdThreads = 32 * kBwdWarps;
 constexpr int kCheckpoint = 0, kSummary = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -45,26 +43,40 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int S> struct BwdShape {
     static constexpr int NS = 4 * S;                           // states, padded
     static constexpr int CW = 32 / S;                          // channels per warp and slot
-    static constexpr int KC = S <= 4 ? 1 : S / 4;              // channel slots per warp
+    static constexpr int KL = S >= 4 ? 2 : 1;                  // channels a lane takes in step
+    static constexpr int T = 8 / KL;                           // steps in registers
+    static constexpr int W = S == 4 ? 2 : 4;                   // scan warps per CTA
+    static constexpr int NH = S == 1 || S == 2 ? 128 : 64;     // helper threads
+    static constexpr int NT = 32 * W + NH;
+    static constexpr int KC = S <= 8 ? 1 : S / 8;              // such groups a warp takes in turn
     static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
-    static constexpr int G = kBwdWarps * CW * KC;              // channels per CTA
-    static constexpr int TT = S == 1 || S >= 16 ? 8 : 16;      // steps per tile
-    static constexpr int NSUB = TT / kSubSteps;
-    static constexpr int EPT = G * TT / kBwdThreads;           // elements per thread and tensor
-    static constexpr int RB = NS + 4;                          // row of B / C in floats
+    static constexpr int G = W * CW * KL * KC;                 // channels per CTA
+    static constexpr int TT = 8;                               // steps per tile
+    static constexpr int NSUB = TT / T;
+    static constexpr int EPT = G * TT / NH;                    // elements per helper and tensor
+    static constexpr int RB = NS;                              // row of B / C in floats
     // shared memory, in floats
+    // one of two staged tiles
     static constexpr int kSt = 4 * G * (TT + 1);               // {delta, delta, delta u, delta u}
     static constexpr int kG = 2 * G * (TT + 1);                // {g, g}
-    static constexpr int RO = TT + 4;                          // row of u, y, s1, s2 in floats
+    static constexpr int RO = TT + 1;                          // row of u, y, s1, s2 in floats
     static constexpr int kU = G * RO;
     static constexpr int kOut = G * RO;                        // one of y, s1, s2
     static constexpr int RQ = TT * RB + 16;                    // one order's copy of B / C: the copies
     static constexpr int kBC = NC * RQ;                        // begin 16 banks apart
-    static constexpr int kPart = kBwdWarps * TT * 2 * NS;
+    static constexpr int kStaged(bool adj) { return kSt + (adj ? kG + kU + 2 * kBC : kBC); }
+    static constexpr int RP = 2 * NS + 8;                      // row of dB, dC of a step
+    static constexpr int kPart = W * TT * RP;
     static constexpr int kPrm = 8 * G;
-    static constexpr int kMask = 4;                            // sequence starts of the tile, as bits
+    static constexpr int kMask = 4;                            // sequence starts of the two tiles, as bits
     static constexpr int kSum = 2 * G * TT;                    // channel-last dD, dbias sums
-    static constexpr int kCarry = KC > 2 ? kBwdThreads * KC * 8 : 0;
+    static constexpr int kCarry = KC > 1 ? 32 * W * KC * KL * 8 : 0;
+    // the place in the CTA of channel kl of lane (warp, cl, j) in group kc. Lanes with odd j
+    // take their two channels the other way round: the sums over a channel's lanes then
+    // exchange the same slot in every lane (reduce_states).
+    static __device__ __forceinline__ int channel(int warp, int kc, int cl, int j, int kl) {
+        return ((warp * KC + kc) * CW + cl) * KL + (KL > 1 && S > 1 ? kl ^ (j & 1) : kl);
+    }
 };
 
 // The order of a lane's 4 states. Slot k of a channel's lane j holds state 4 j + (k ^ q),
@@ -73,10 +85,11 @@ template <int S> struct BwdShape {
 // two that differ in bit 0 each other's odd state in the even slot: the sums over a warp's
 // channels exchange the same slots in every lane, without a select per value (measured with
 // the selects: 33 instructions per channel, step and state; without: see scan_bwd_kernel).
-// Everything the kernels pass to one another in scratch memory is in this order.
+// Everything the kernels pass to one another in scratch memory is in this order. A lane's two
+// channels (KL) have the same order.
 template <int S>
 __device__ __forceinline__ int slot_order(int d) {
-    return d & (BwdShape<S>::NC - 1);                          // CTAs begin at multiples of 32 / S
+    return d / BwdShape<S>::KL & (BwdShape<S>::NC - 1);        // CTAs begin at multiples of G
 }
 
 // One tile's inputs as they lie in global memory, copied to shared memory a tile ahead of
@@ -194,39 +207,53 @@ __device__ __forceinline__ float sigmoidf_(float v) {
     return __fdividef(1.f, 1.f + ex2(-v * kLog2e));
 }
 
-// Sum over the S lanes of a channel of 8 values a lane (one per step): every level adds
-// the partner's half of the values still carried. Afterwards a lane holds 8 / min(S, 8)
-// sums, those of the steps from reduce8_first(lane).
-template <int S>
-__device__ __forceinline__ void reduce8(float (&v)[8], int lane) {
-    int cnt = 8;
+// Sums over the S lanes of a channel of 8 values a lane, [channel][step]. With two channels
+// the first level trades the second slot (lanes with odd j hold the channels the other way
+// round); every further level adds the partner's half of the steps still carried.
+// Afterwards a lane holds kept() sums of its first slot's channel, from step first() on.
+template <int S> struct StateSums {
+    using H = BwdShape<S>;
+    static constexpr bool kTrade = H::KL == 2 && S > 1;
+    static constexpr int levels() {
+        int n = 0;
+        for (int w = kTrade ? 2 : 1; w < S; w *= 2) ++n;
+        return n;
+    }
+    static constexpr int kept() { return levels() >= (H::T == 8 ? 3 : 2) ? 1 : H::T >> levels(); }
+    static __device__ __forceinline__ void sum(float (&v)[8], int lane) {
+        if constexpr (kTrade) {
 #pragma unroll
-    for (int w = 1; w < S; w *= 2) {
-        if (cnt > 1) {
-            cnt /= 2;
-            const bool up = lane & w;
+            for (int i = 0; i < H::T; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[H::T + i], 1);
+        }
+        int cnt = H::T;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < cnt) {
-                    const float send = up ? v[k] : v[k + cnt];
-                    const float keep = up ? v[k + cnt] : v[k];
-                    v[k] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-                }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+        for (int w = kTrade ? 2 : 1; w < S; w *= 2) {
+            if (cnt > 1) {
+                cnt /= 2;
+                const bool up = lane & w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < cnt) {
+                        const float send = up ? v[k] : v[k + cnt];
+                        const float keep = up ? v[k + cnt] : v[k];
+                        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                    }
+            } else {
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+            }
         }
     }
-}
-template <int S>
-__device__ __forceinline__ int reduce8_first(int lane) {
-    int off = 0, cnt = 8;
+    static __device__ __forceinline__ int first(int lane) {
+        int off = 0, cnt = H::T;
 #pragma unroll
-    for (int w = 1; w < S && w < 8; w *= 2) {
-        cnt /= 2;
-        off += (lane & w) ? cnt : 0;
+        for (int w = kTrade ? 2 : 1; w < S; w *= 2)
+            if (cnt > 1) {
+                cnt /= 2;
+                off += (lane & w) ? cnt : 0;
+            }
+        return off;
     }
-    return off;
-}
+};
 
 // Sum over the first NC channels of a lane's 4 values (one per state slot): each level
 // adds the partner's other half. Leaves 4 / NC values, of slots 0, 4 / NC, ...
@@ -249,35 +276,40 @@ __device__ __forceinline__ void reduce_slots(const uint64_t (&v)[2], float* r) {
     }
 }
 
-// Sum over the remaining 32 / S / 4 groups of channels of 8 values (one per step): as
-// reduce8, over the upper lane bits. A lane keeps 8 / (8 / S) of them from
-// reduce_groups_first(lane).
-template <int S>
-__device__ __forceinline__ void reduce_groups(float (&v)[8], int lane) {
-    int cnt = 8;
-#pragma unroll
-    for (int w = 4 * S; w < 32; w *= 2) {
-        cnt /= 2;
-        const bool up = lane & w;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < cnt) {
-                const float send = up ? v[k] : v[k + cnt];
-                const float keep = up ? v[k + cnt] : v[k];
-                v[k] = keep + __shfl_xor_sync(0xffffffffu, send, w);
-            }
+// Sum over the remaining 32 / S / 4 groups of channels of T values (one per step), over the
+// upper lane bits: a lane keeps kept() of them from step first() on.
+template <int S> struct GroupSums {
+    static constexpr int T = BwdShape<S>::T;
+    static constexpr int kept() {
+        int n = T;
+        for (int w = 4 * S; w < 32; w *= 2) n /= 2;
+        return n;
     }
-}
-template <int S>
-__device__ __forceinline__ int reduce_groups_first(int lane) {
-    int off = 0, cnt = 8;
+    static __device__ __forceinline__ void sum(float (&v)[T], int lane) {
+        int cnt = T;
 #pragma unroll
-    for (int w = 4 * S; w < 32; w *= 2) {
-        cnt /= 2;
-        off += (lane & w) ? cnt : 0;
+        for (int w = 4 * S; w < 32; w *= 2) {
+            cnt /= 2;
+            const bool up = lane & w;
+#pragma unroll
+            for (int k = 0; k < T / 2; ++k)
+                if (k < cnt) {
+                    const float send = up ? v[k] : v[k + cnt];
+                    const float keep = up ? v[k + cnt] : v[k];
+                    v[k] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                }
+        }
     }
-    return off;
-}
+    static __device__ __forceinline__ int first(int lane) {
+        int off = 0, cnt = T;
+#pragma unroll
+        for (int w = 4 * S; w < 32; w *= 2) {
+            cnt /= 2;
+            off += (lane & w) ? cnt : 0;
+        }
+        return off;
+    }
+};
 
 // Where a thread's run of EPT elements of a tile lies: along the steps of one channel, or
 // (channel-last) along the channels of one step.
@@ -301,7 +333,7 @@ template <int S, bool CL> struct BwdRun {
 template <int S>
 __device__ __forceinline__ void load_prm(const BwdParams& p, int d0, float* prm) {
     using H = BwdShape<S>;
-    for (int c = threadIdx.x; c < H::G; c += kBwdThreads) {
+    for (int c = threadIdx.x; c < H::G; c += H::NT) {
         const int d = d0 + c;
         const bool in = d < p.dim;
 #pragma unroll
@@ -349,7 +381,7 @@ template <typename T, int S, bool CL, bool Q8, bool ADJ> struct BwdCopies {
     static constexpr int NY = CL ? TT * PY : H::G * PY;
     // x, halo, delta, B (and with ADJ z, dout, C)
     static constexpr int COUNT = NX + NH + NQ + NB + (ADJ ? NQ + NY + NB : 0);
-    static constexpr int PER = (COUNT + kBwdThreads - 1) / kBwdThreads;
+    static constexpr int PER = (COUNT + H::NH - 1) / H::NH;
 
     static __device__ BwdCopy make(const BwdParams& p, int b, int d0, int id) {
         const int have = p.dim - d0;
@@ -411,7 +443,7 @@ template <typename T, int S, bool CL, bool Q8, bool ADJ> struct BwdCopies {
 
 // The plain form of the same copies, element by element, for rows that are not aligned.
 template <typename T, int S, bool CL, bool Q8, bool ADJ>
-__device__ __forceinline__ void fetch_plain(const BwdParams& p, int b, int d0, int t0, uint8_t* raw) {
+__device__ __forceinline__ void fetch_plain(const BwdParams& p, int hid, int b, int d0, int t0, uint8_t* raw) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
     constexpr int TT = H::TT, ES = R::ES, EQ = Q8 ? 1 : ES;
@@ -428,7 +460,7 @@ __device__ __forceinline__ void fetch_plain(const BwdParams& p, int b, int d0, i
         constexpr int e = decltype(size)::value;
         const uint8_t* src = static_cast<const uint8_t*>(ptr) + (int64_t)b * st.b * e;
 #pragma unroll 2
-        for (int i = threadIdx.x; i < rows * width; i += kBwdThreads) {
+        for (int i = hid; i < rows * width; i += H::NH) {
             const int r = i / width, k = i % width, t = t0 - lead + r;
             const int pos = CL ? (p.reverse ? L - 1 - t : t) : pos0 + k, c = CL ? k : r;
             const bool in = c < count && pos >= 0 && pos < L;
@@ -443,7 +475,7 @@ __device__ __forceinline__ void fetch_plain(const BwdParams& p, int b, int d0, i
     } else {
         copy(p.x.p, p.x.s, d0, have, H::G, TT, 0, raw + R::X + (p.reverse ? 0 : 16), R::kXRow, sq);
         const uint8_t* src = static_cast<const uint8_t*>(p.x.p) + ((int64_t)b * p.x.s.b + (int64_t)d0 * p.x.s.c) * EQ;
-        for (int i = threadIdx.x; i < (p.conv_w ? H::G * 4 : 0); i += kBwdThreads) {
+        for (int i = hid; i < (p.conv_w ? H::G * 4 : 0); i += H::NH) {
             const int r = i / 4, o = i % 4 - 4, t = t0 + o, pos = p.reverse ? L - 1 - t : t;
             put(raw + R::X + r * R::kXRow, p.reverse ? TT - 1 - o : 16 / EQ + o,
                 src + ((int64_t)r * p.x.s.c + pos) * EQ, r < have && pos >= 0 && pos < L, sq);
@@ -462,7 +494,7 @@ __device__ __forceinline__ void fetch_plain(const BwdParams& p, int b, int d0, i
 // dout, C. Asynchronous copies where the host found every row aligned to their units
 // (p.async), from the CTA's table; else plain loads.
 template <typename T, int S, bool CL, bool Q8, bool ADJ>
-__device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* table, int b, int d0, int t0,
+__device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* table, int hid, int b, int d0, int t0,
                                            uint8_t* raw) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
@@ -472,7 +504,7 @@ __device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* ta
         const uint32_t dst = smem_u32(raw);
 #pragma unroll
         for (int k = 0; k < K::PER; ++k) {
-            const int id = threadIdx.x + k * kBwdThreads;
+            const int id = hid + k * H::NH;
             if (id >= K::COUNT) break;
             const BwdCopy c = table[id];
             const int pos = CL ? (p.reverse ? L - 1 - (t0 + c.at) : t0 + c.at) : pos0 + c.at;
@@ -486,13 +518,13 @@ __device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* ta
             else cp_async<16>(dst + c.dst, src, n);
         }
     } else {
-        fetch_plain<T, S, CL, Q8, ADJ>(p, b, d0, t0, raw);
+        fetch_plain<T, S, CL, Q8, ADJ>(p, hid, b, d0, t0, raw);
     }
     if constexpr (Q8) {
         // a tile and its halo span at most two blocks of 64 positions: both their scales
         const int have = p.dim - d0, last = (L - 1) / kBlock8;
         const int lo = min(max(pos0 - 3, 0) / kBlock8, last), hi = min(max(pos0 + H::TT + 2, 0) / kBlock8, last);
-        for (int i = threadIdx.x; i < 6 * H::G; i += kBwdThreads) {
+        for (int i = hid; i < 6 * H::G; i += H::NH) {
             const int c = i % H::G, which = i / H::G, k = which / 2;
             const ActIn& a = k == 0 ? p.x : k == 1 ? p.dt : p.z;
             const bool in = c < have && a.scale && (k < 2 || ADJ);
@@ -502,7 +534,7 @@ __device__ __forceinline__ void fetch_tile(const BwdParams& p, const BwdCopy* ta
             cp_async<4>(smem_u32(raw + R::SC + 4 * i), q, in ? 4 : 0);
         }
     }
-    if (p.since && threadIdx.x == 0) cp_async<H::TT>(smem_u32(raw + R::SINCE), p.since + t0, H::TT);
+    if (p.since && hid == 0) cp_async<H::TT>(smem_u32(raw + R::SINCE), p.since + t0, H::TT);
     cp_async_commit();
 }
 
@@ -577,18 +609,29 @@ __device__ __forceinline__ void take(const BwdParams& p, const uint8_t* raw, int
     }
 }
 
+// out[i] = f(in[i]), two at a time.
+template <int E, typename F>
+__device__ __forceinline__ void each_pair(float (&out)[E], const float (&in)[E], F&& f) {
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+        const float2 v = upk2(f(pk2(in[i], in[i + 1])));
+        out[i] = v.x;
+        out[i + 1] = v.y;
+    }
+}
+
 // Turn a tile's raw inputs into what the recurrences take: delta and delta u (each twice, as
 // the pairs they take) per channel and step, g and u where ADJ, and the rows of B (and C
 // where ADJ) in each order of the states. Steps past the end and channels past dim get
 // zeros: a = 1 and no input, which leave both recurrences where they are.
 template <typename T, int S, bool CL, bool Q8, bool ADJ>
-__device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, int t0, const uint8_t* raw,
+__device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, int d0, int t0, const uint8_t* raw,
                                            const float* prm, float4* st, float2* gs, float* us,
                                            float* Bs, float* Cs, uint32_t* mask) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
     constexpr int E = H::EPT;
-    const int tid = threadIdx.x, L = p.seqlen;
+    const int tid = hid, L = p.seqlen;
     const BwdRun<S, CL> r(tid);
     const int d = d0 + r.ch, t = t0 + r.tl;
     // valid elements of the run: [0, hi)
@@ -664,8 +707,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) u[i] = silu(acc[i]);
+        each_pair(u, acc, [](uint64_t v) { return silu2(v); });
     }
     take<T, S, CL, Q8>(p, raw, 1, r, t0, dt);
     if constexpr (ADJ) {
@@ -673,14 +715,18 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
         if (p.z.p) {
             float z[E];
             take<T, S, CL, Q8>(p, raw, 2, r, t0, z);
+            each_pair(z, z, [](uint64_t v) { return silu2(v); });
 #pragma unroll
-            for (int i = 0; i < E; ++i) g[i] *= silu(z[i]);
+            for (int i = 0; i < E; ++i) g[i] *= z[i];
         }
     }
 #pragma unroll
+    for (int i = 0; i < E; ++i) dt[i] += prm[r.c(i) * 8 + 5];
+    // past 20 the softplus is its argument to fp32 by itself
+    if (p.softplus) each_pair(dt, dt, [](uint64_t v) { return softplus2(v); });
+#pragma unroll
     for (int i = 0; i < E; ++i) {
-        const float raw_dt = dt[i] + prm[r.c(i) * 8 + 5];
-        float dl = p.softplus ? (raw_dt > 20.f ? raw_dt : softplus(raw_dt)) : raw_dt;
+        float dl = dt[i];
         if (i >= hi) {
             dl = u[i] = 0.f;
             if (ADJ) g[i] = 0.f;
@@ -700,7 +746,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int b, int d0, in
     }
     // rows of B and C: the 4 states of a lane at a step, once per order
 #pragma unroll
-    for (int k = tid; k < S * H::TT * (ADJ ? 2 : 1); k += kBwdThreads) {
+    for (int k = tid; k < S * H::TT * (ADJ ? 2 : 1); k += H::NH) {
         const int jj = k % S, tl = k / S % H::TT;
         const bool isC = ADJ && k >= S * H::TT;
         const T* src = reinterpret_cast<const T*>(raw + (isC ? R::C : R::B));
@@ -749,19 +795,19 @@ __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint
     }
 }
 
-// Decays of the kSubSteps steps from row, zero at the sequence starts in mask.
-template <bool HEADS>
+// Decays and delta u of the T steps from row, the decays zero at the sequence starts in mask.
+template <bool HEADS, int T>
 __device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float4* row, uint32_t mask,
-                                       uint64_t (&a)[kSubSteps][2], uint64_t (&du2)[kSubSteps]) {
+                                       uint64_t (&a)[T][2], uint64_t (&du2)[T]) {
 #pragma unroll
-    for (int i = 0; i < kSubSteps; ++i) {
+    for (int i = 0; i < T; ++i) {
         const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(row + i);
         decay<HEADS>(A2, s.x, a[i]);
         du2[i] = s.y;
     }
     if (mask) {
 #pragma unroll
-        for (int i = 0; i < kSubSteps; ++i)
+        for (int i = 0; i < T; ++i)
             if (mask >> i & 1) a[i][0] = a[i][1] = 0;
     }
 }
@@ -795,18 +841,40 @@ __device__ __forceinline__ int64_t ns_off(const BwdParams& p, int64_t row, int d
     return (row * p.dim + d) * (4 * S) + 4 * j;
 }
 
+// The arrays of a staged tile (one of two).
+template <int S> struct BwdStaged {
+    using H = BwdShape<S>;
+    float4* st;
+    float2* gs;
+    float *us, *Bs, *Cs;
+    __device__ __forceinline__ BwdStaged(float* sm, bool adj) {
+        st = reinterpret_cast<float4*>(sm);
+        gs = reinterpret_cast<float2*>(sm + H::kSt);
+        us = sm + H::kSt + (adj ? H::kG : 0);
+        Bs = us + (adj ? H::kU : 0);
+        Cs = Bs + H::kBC;
+    }
+    __device__ __forceinline__ BwdStaged at(int n, int size) const {
+        BwdStaged r = *this;
+        r.st += n * size / 4;
+        r.gs += n * size / 2;
+        r.us += n * size;
+        r.Bs += n * size;
+        r.Cs += n * size;
+        return r;
+    }
+};
+
 // The forward pass: checkpoints of the state (MODE kCheckpoint), or a segment's summary.
 template <typename T, int S, bool CL, bool Q8, bool HEADS, int MODE>
-__global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr bool SUM = MODE == kSummary;
+    constexpr int KL = H::KL, ST = H::T;
     extern __shared__ __align__(16) float sm[];
-    float4* st = reinterpret_cast<float4*>(sm);
-    float2* gs = reinterpret_cast<float2*>(sm + H::kSt);
-    float* us = sm + H::kSt + (SUM ? H::kG : 0);
-    float* Bs = us + (SUM ? H::kU : 0);
-    float* Cs = Bs + H::kBC;
-    float* prm = Cs + (SUM ? H::kBC : 0);
+    constexpr int kStaged = H::kStaged(SUM);
+    const BwdStaged<S> staged(sm, SUM);
+    float* prm = sm + 2 * kStaged;
     uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
     uint8_t* raw = reinterpret_cast<uint8_t*>(prm + H::kPrm + H::kMask);
     constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
@@ -818,71 +886,103 @@ __global__ void __launch_bounds__(kBwdThreads) scan_bwd_states_kernel(const BwdP
     const int tb = seg * p.seg_len, te = min(p.seqlen, tb + p.seg_len);
     const int64_t row = (int64_t)seg * p.batch + b;
     load_prm<S>(p, d0, prm);
-    uint64_t h[H::KC][2], A2[H::KC][2], R[H::KC][2], P[H::KC][2];
-#pragma unroll
-    for (int kc = 0; kc < H::KC; ++kc) {
-        const int d = d0 + (warp * H::KC + kc) * H::CW + cl;
-        load_A<S, HEADS>(p, d, j, A2[kc]);
-        R[kc][0] = R[kc][1] = 0;
-        P[kc][0] = P[kc][1] = pk2(1.f, 1.f);
-        h[kc][0] = h[kc][1] = 0;
-        if (!SUM && seg == 0) load_state<S>(p, p.h0, b, d, j, h[kc]);
-        if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc]);
+    __syncthreads();
+    const int ntiles = (te - tb + H::TT - 1) / H::TT;
+
+    if (warp >= H::W) {                                        // helper: tile n + 1 while n is scanned
+        const int hid = tid - 32 * H::W;
+        auto fetch = [&](int n) {
+            fetch_tile<T, S, CL, Q8, SUM>(p, table, hid, b, d0, tb + n * H::TT, raw + (n & 1) * kRaw);
+        };
+        auto stage = [&](int n) {
+            const BwdStaged<S> to = staged.at(n & 1, kStaged);
+            stage_tile<T, S, CL, Q8, SUM>(p, hid, b, d0, tb + n * H::TT, raw + (n & 1) * kRaw, prm, to.st, to.gs,
+                                          to.us, to.Bs, to.Cs, mask + (n & 1));
+        };
+        if (p.async)                                           // a thread reads back its own entries
+            for (int k = hid; k < K::COUNT; k += H::NH) table[k] = K::make(p, b, d0, k);
+        fetch(0);
+        for (int n = -1; n < ntiles; ++n) {
+            cp_async_wait();
+            named_bar_sync(1, H::NH);                          // tile n + 1 is here, n has been staged
+            if (n + 2 < ntiles) fetch(n + 2);
+            if (n + 1 < ntiles) stage(n + 1);
+            __syncthreads();
+        }
+        return;
     }
-    if (p.async)                                               // a thread reads back its own entries
-        for (int k = tid; k < K::COUNT; k += kBwdThreads) table[k] = K::make(p, b, d0, k);
-    fetch_tile<T, S, CL, Q8, SUM>(p, table, b, d0, tb, raw);
-    int buf = 0;
-    for (int t0 = tb; t0 < te; t0 += H::TT, buf ^= 1) {
-        cp_async_wait();
-        __syncthreads();                                       // this tile is here, the last one used
-        if (t0 + H::TT < te) fetch_tile<T, S, CL, Q8, SUM>(p, table, b, d0, t0 + H::TT, raw + (buf ^ 1) * kRaw);
-        stage_tile<T, S, CL, Q8, SUM>(p, b, d0, t0, raw + buf * kRaw, prm, st, gs, us, Bs, Cs, mask);
-        __syncthreads();
-        const uint32_t starts = *mask;
+
+    uint64_t h[H::KC][KL][2], A2[H::KC][KL][2], R[H::KC][KL][2], P[H::KC][KL][2];
+#pragma unroll
+    for (int kc = 0; kc < H::KC; ++kc)
+#pragma unroll
+        for (int kl = 0; kl < KL; ++kl) {
+            const int d = d0 + H::channel(warp, kc, cl, j, kl);
+            load_A<S, HEADS>(p, d, j, A2[kc][kl]);
+            R[kc][kl][0] = R[kc][kl][1] = 0;
+            P[kc][kl][0] = P[kc][kl][1] = pk2(1.f, 1.f);
+            h[kc][kl][0] = h[kc][kl][1] = 0;
+            if (!SUM && seg == 0) load_state<S>(p, p.h0, b, d, j, h[kc][kl]);
+            if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc][kl]);
+        }
+    __syncthreads();                                           // tile 0 is staged
+    for (int n = 0; n < ntiles; ++n) {
+        const int t0 = tb + n * H::TT;
+        const BwdStaged<S> in = staged.at(n & 1, kStaged);
+        const uint32_t starts = mask[n & 1];
 #pragma unroll
         for (int kc = 0; kc < H::KC; ++kc) {
-            const int c = (warp * H::KC + kc) * H::CW + cl, d = d0 + c, q = slot_order<S>(d);
+            const int q = slot_order<S>(H::channel(warp, kc, cl, 0, 0));
 #pragma unroll 1
             for (int sub = 0; sub < H::NSUB; ++sub) {
-                if (!SUM && d < p.dim)
-                    stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / kSubSteps + sub, d, j), h[kc]);
-                const int o = c * (H::TT + 1) + sub * kSubSteps;
-                const float* Br = Bs + q * H::RQ + sub * kSubSteps * H::RB + 4 * j;
-                const float* Cr = Cs + q * H::RQ + sub * kSubSteps * H::RB + 4 * j;
-                uint64_t a[kSubSteps][2], du2[kSubSteps];
-                decays<HEADS>(A2[kc], st + o, starts >> (sub * kSubSteps) & 255, a, du2);
+                const float* Br = in.Bs + q * H::RQ + sub * ST * H::RB + 4 * j;
+                const float* Cr = in.Cs + q * H::RQ + sub * ST * H::RB + 4 * j;
+                uint64_t a[KL][ST][2], du2[KL][ST];
+                int so[KL];
 #pragma unroll
-                for (int i = 0; i < kSubSteps; ++i) {
-                    uint64_t bv[2], cv[2], g2 = 0;
+                for (int kl = 0; kl < KL; ++kl) {
+                    const int c = H::channel(warp, kc, cl, j, kl);
+                    so[kl] = c * (H::TT + 1) + sub * ST;
+                    if (!SUM && d0 + c < p.dim)
+                        stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / ST + sub, d0 + c, j), h[kc][kl]);
+                    decays<HEADS, ST>(A2[kc][kl], in.st + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
+                }
+#pragma unroll
+                for (int i = 0; i < ST; ++i) {
+                    uint64_t bv[2], cv[2];
                     ldpair(Br + i * H::RB, bv);
-                    if (SUM) {
-                        ldpair(Cr + i * H::RB, cv);
-                        g2 = *reinterpret_cast<const uint64_t*>(gs + o + i);
-                    }
+                    if (SUM) ldpair(Cr + i * H::RB, cv);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        h[kc][k] = fma2(a[i][k], h[kc][k], mul2(du2[i], bv[k]));
-                        if (SUM) {
-                            P[kc][k] = mul2(P[kc][k], a[i][k]);
-                            R[kc][k] = fma2(P[kc][k], mul2(g2, cv[k]), R[kc][k]);
+                    for (int kl = 0; kl < KL; ++kl) {
+                        uint64_t g2 = 0;
+                        if (SUM) g2 = *reinterpret_cast<const uint64_t*>(in.gs + so[kl] + i);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            h[kc][kl][k] = fma2(a[kl][i][k], h[kc][kl][k], mul2(du2[kl][i], bv[k]));
+                            if (SUM) {
+                                P[kc][kl][k] = mul2(P[kc][kl][k], a[kl][i][k]);
+                                R[kc][kl][k] = fma2(P[kc][kl][k], mul2(g2, cv[k]), R[kc][kl][k]);
+                            }
                         }
                     }
                 }
             }
         }
+        __syncthreads();                                       // tile n is done, n + 1 staged
     }
     if (SUM) {
 #pragma unroll
-        for (int kc = 0; kc < H::KC; ++kc) {
-            const int d = d0 + (warp * H::KC + kc) * H::CW + cl;
-            if (d < p.dim) {
-                const int64_t o = ns_off<S>(p, row, d, j);
-                stpair(p.sumP + o, P[kc]);
-                stpair(p.sumS + o, h[kc]);
-                stpair(p.sumR + o, R[kc]);
+        for (int kc = 0; kc < H::KC; ++kc)
+#pragma unroll
+            for (int kl = 0; kl < KL; ++kl) {
+                const int d = d0 + H::channel(warp, kc, cl, j, kl);
+                if (d < p.dim) {
+                    const int64_t o = ns_off<S>(p, row, d, j);
+                    stpair(p.sumP + o, P[kc][kl]);
+                    stpair(p.sumS + o, h[kc][kl]);
+                    stpair(p.sumR + o, R[kc][kl]);
+                }
             }
-        }
     }
 }
 
@@ -914,20 +1014,15 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
 
 // The backward sweep.
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
-__global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) scan_bwd_kernel(const BwdParams p) {
     using H = BwdShape<S>;
-    constexpr int KC = H::KC, TT = H::TT, E = H::EPT;
-    constexpr bool REGS = KC <= 2;                             // m and dA of every slot in registers
+    constexpr int KC = H::KC, KL = H::KL, ST = H::T, TT = H::TT, E = H::EPT;
+    constexpr bool REGS = KC == 1;                             // m and dA in registers, else carried over
     extern __shared__ __align__(16) float sm[];
-    float4* st = reinterpret_cast<float4*>(sm);
-    float2* gs = reinterpret_cast<float2*>(sm + H::kSt);
-    float* us = sm + H::kSt + H::kG;
-    float* ys = us + H::kU;
-    float* s1s = ys + H::kOut;
-    float* s2s = s1s + H::kOut;
-    float* Bs = s2s + H::kOut;
-    float* Cs = Bs + H::kBC;
-    float* part = Cs + H::kBC;
+    constexpr int kStaged = H::kStaged(true);
+    const BwdStaged<S> staged(sm, true);
+    float* outs = sm + 2 * kStaged;                            // y, s1, s2 of two tiles
+    float* part = outs + 6 * H::kOut;
     float* prm = part + H::kPart;
     uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
     float* carry = prm + H::kPrm + H::kMask;
@@ -935,7 +1030,7 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
     uint8_t* raw = reinterpret_cast<uint8_t*>(sums + (CL ? H::kSum : 0));
     constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
     using K = BwdCopies<T, S, CL, Q8, true>;
-    BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 2 * kRaw);
+    BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 3 * kRaw);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int j = lane % S, cl = lane / S;
     const int b = blockIdx.y, d0 = blockIdx.x * H::G, seg = blockIdx.z;
@@ -943,184 +1038,50 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
     const int64_t row = (int64_t)seg * p.batch + b;
     load_prm<S>(p, d0, prm);
 
-    uint64_t m[REGS ? KC : 1][2], dA[REGS ? KC : 1][2], A2[REGS ? KC : 1][2];
-#pragma unroll
-    for (int kc = 0; kc < KC; ++kc) {
-        const int d = d0 + (warp * KC + kc) * H::CW + cl;
-        const int r = REGS ? kc : 0;
-        dA[r][0] = dA[r][1] = 0;
-        m[r][0] = m[r][1] = 0;
-        if (te == L) load_state<S>(p, p.dhl, b, d, j, m[r]);
-        else if (d < p.dim) ldpair(p.sumR + ns_off<S>(p, row, d, j), m[r]);
-        if constexpr (REGS) {
-            load_A<S, HEADS>(p, d, j, A2[r]);
-        } else {
-            stpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
-            stpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
-        }
-    }
-    const BwdRun<S, CL> run(tid);
-    float dD = 0.f, dBias = 0.f;
-    if constexpr (CL) {
-        for (int k = tid; k < H::kSum; k += kBwdThreads) sums[k] = 0.f;
-    }
-
     const int ntiles = (te - tb + TT - 1) / TT;
-    // the states before sub-tile `sub` of a tile, for slot kc; fetched one use ahead
-    auto load_ckpt = [&](int tile, int sub, int kc, uint64_t (&v)[2]) {
-        const int d = d0 + (warp * KC + kc) * H::CW + cl;
-        if (d < p.dim)
-            ldpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + (tb + tile * TT) / kSubSteps + sub, d, j), v);
-    };
-    uint64_t hn[2] = {0, 0};
-    load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
-    if (p.async)                                               // a thread reads back its own entries
-        for (int k = tid; k < K::COUNT; k += kBwdThreads) table[k] = K::make(p, b, d0, k);
-    fetch_tile<T, S, CL, Q8, true>(p, table, b, d0, tb + (ntiles - 1) * TT, raw);
-    int buf = 0;
-    for (int tile = ntiles - 1; tile >= 0; --tile, buf ^= 1) {
-        const int t0 = tb + tile * TT;
-        const uint8_t* cur = raw + buf * kRaw;
-        cp_async_wait();
-        __syncthreads();                                       // this tile is here, the last one used
-        if (tile > 0) fetch_tile<T, S, CL, Q8, true>(p, table, b, d0, t0 - TT, raw + (buf ^ 1) * kRaw);
-        stage_tile<T, S, CL, Q8, true>(p, b, d0, t0, cur, prm, st, gs, us, Bs, Cs, mask);
-        __syncthreads();
-        const uint32_t starts = *mask;
-#pragma unroll 1
-        for (int sub = H::NSUB - 1; sub >= 0; --sub) {
-            constexpr int PT = 4 / H::NC;                      // values left per step
-            float rB[8 * PT], rC[8 * PT];
-            if constexpr (KC > 1) {
-#pragma unroll
-                for (int i = 0; i < 8 * PT; ++i) rB[i] = rC[i] = 0.f;
-            }
-            constexpr int UNR = REGS ? KC : 1;
-#pragma unroll UNR
-            for (int kc = 0; kc < KC; ++kc) {
-                const int c = (warp * KC + kc) * H::CW + cl, d = d0 + c, sq = slot_order<S>(d);
-                const int r = REGS ? kc : 0;
-                const uint64_t h0[2] = {hn[0], hn[1]};
-                if (kc + 1 < KC) load_ckpt(tile, sub, kc + 1, hn);
-                else if (sub > 0) load_ckpt(tile, sub - 1, 0, hn);
-                else if (tile > 0) load_ckpt(tile - 1, H::NSUB - 1, 0, hn);
-                if constexpr (!REGS) {
-                    load_A<S, HEADS>(p, d, j, A2[0]);
-                    ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
-                    ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
-                }
-                const int so = c * (TT + 1) + sub * kSubSteps;
-                const float* Br = Bs + sq * H::RQ + sub * kSubSteps * H::RB + 4 * j;
-                const float* Cr = Cs + sq * H::RQ + sub * kSubSteps * H::RB + 4 * j;
-                uint64_t a[kSubSteps][2], h[kSubSteps][2];
-                {
-                    uint64_t du2[kSubSteps];
-                    decays<HEADS>(A2[r], st + so, starts >> (sub * kSubSteps) & 255, a, du2);
-#pragma unroll
-                    for (int i = 0; i < kSubSteps; ++i) {
-                        uint64_t bv[2];
-                        ldpair(Br + i * H::RB, bv);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            h[i][k] = fma2(a[i][k], i ? h[i ? i - 1 : 0][k] : h0[k], mul2(du2[i], bv[k]));
-                    }
-                }
-                float y[8], s1[8], s2[8];
-#pragma unroll
-                for (int i = kSubSteps - 1; i >= 0; --i) {
-                    const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(st + so + i);
-                    const uint64_t g2 = *reinterpret_cast<const uint64_t*>(gs + so + i);
-                    uint64_t bv[2], cv[2], lam[2], q[2], tb2[2], tc2[2];
-                    ldpair(Br + i * H::RB, bv);
-                    ldpair(Cr + i * H::RB, cv);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        lam[k] = fma2(g2, cv[k], m[r][k]);
-                        m[r][k] = mul2(a[i][k], lam[k]);
-                        q[k] = mul2(m[r][k], i ? h[i ? i - 1 : 0][k] : h0[k]);
-                        dA[r][k] = fma2(q[k], s.x, dA[r][k]);
-                        tb2[k] = mul2(lam[k], s.y);
-                        tc2[k] = mul2(g2, h[i][k]);
-                    }
-                    float vb[PT], vc[PT];
-                    reduce_slots<S>(tb2, vb);
-                    reduce_slots<S>(tc2, vc);
-#pragma unroll
-                    for (int k = 0; k < PT; ++k) {
-                        rB[i * PT + k] = KC > 1 ? rB[i * PT + k] + vb[k] : vb[k];
-                        rC[i * PT + k] = KC > 1 ? rC[i * PT + k] + vc[k] : vc[k];
-                    }
-                    const float2 fy = upk2(fma2(cv[1], h[i][1], mul2(cv[0], h[i][0])));
-                    const float2 f1 = upk2(fma2(bv[1], lam[1], mul2(bv[0], lam[0])));
-                    y[i] = fy.x + fy.y;
-                    s1[i] = f1.x + f1.y;
-                    if constexpr (HEADS) {
-                        const float2 f2 = upk2(add2(q[0], q[1]));
-                        s2[i] = lo2(A2[r][0]) * (f2.x + f2.y);
-                    } else {
-                        const float2 f2 = upk2(fma2(q[1], A2[r][1], mul2(q[0], A2[r][0])));
-                        s2[i] = f2.x + f2.y;
-                    }
-                }
-                reduce8<S>(y, lane);
-                reduce8<S>(s1, lane);
-                reduce8<S>(s2, lane);
-                if (j < 8) {
-                    const int o = c * H::RO + sub * kSubSteps + reduce8_first<S>(lane);
-                    constexpr int CNT = S >= 8 ? 1 : 8 / S;
-#pragma unroll
-                    for (int k = 0; k < CNT; ++k) {
-                        ys[o + k] = y[k];
-                        s1s[o + k] = s1[k];
-                        s2s[o + k] = s2[k];
-                    }
-                }
-                if constexpr (!REGS) {
-                    stpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
-                    stpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
-                }
-            }
-            const int sq = slot_order<S>(cl);
-            if constexpr (PT == 1) {
-                reduce_groups<S>(rB, lane);
-                reduce_groups<S>(rC, lane);
-                const int first = reduce_groups_first<S>(lane);
-                constexpr int CNT = S >= 8 ? 8 : S;            // 8 steps over 8 / S groups
-#pragma unroll
-                for (int k = 0; k < CNT; ++k) {
-                    float* o = part + ((warp * TT + sub * kSubSteps + first + k) * 2) * H::NS + 4 * j + sq;
-                    o[0] = rB[k];
-                    o[H::NS] = rC[k];
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8 * PT; ++k) {             // slot k % PT * NC of step k / PT
-                    float* o = part + ((warp * TT + sub * kSubSteps + k / PT) * 2) * H::NS + 4 * j +
-                               (k % PT * H::NC ^ sq);
-                    o[0] = rB[k];
-                    o[H::NS] = rC[k];
-                }
-            }
+    __syncthreads();
+
+    if (warp >= H::W) {
+        // Helper. While tile n (counted from the segment's end) is scanned: the gradients of
+        // tile n - 1, then tile n + 1 into the staged tile that n - 1 leaves.
+        const int hid = tid - 32 * H::W;
+        const BwdRun<S, CL> run(hid);
+        float dD = 0.f, dBias = 0.f;
+        if constexpr (CL) {
+            for (int k = hid; k < H::kSum; k += H::NH) sums[k] = 0.f;
         }
-        __syncthreads();
-        // the tile's gradients, one run per thread
-        {
+        auto start = [&](int n) { return tb + (ntiles - 1 - n) * TT; };
+        auto fetch = [&](int n) {
+            fetch_tile<T, S, CL, Q8, true>(p, table, hid, b, d0, start(n), raw + n % 3 * kRaw);
+        };
+        auto stage = [&](int n) {
+            const BwdStaged<S> to = staged.at(n & 1, kStaged);
+            stage_tile<T, S, CL, Q8, true>(p, hid, b, d0, start(n), raw + n % 3 * kRaw, prm, to.st, to.gs, to.us,
+                                           to.Bs, to.Cs, mask + (n & 1));
+        };
+        // the gradients of a tile, one run per thread
+        auto finish = [&](int n) {
+            const int t0 = start(n);
+            const BwdStaged<S> in = staged.at(n & 1, kStaged);
+            const uint8_t* from = raw + n % 3 * kRaw;
+            const float* ys = outs + (n & 1) * 3 * H::kOut;
+            const float *s1s = ys + H::kOut, *s2s = s1s + H::kOut;
             const int d = d0 + run.ch, t = t0 + run.tl;
             const int pos = p.reverse ? L - 1 - t : t;
             const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
             if (hi > 0) {
                 float dt[E], z[E], dy[E], du[E], ddt[E], dz[E];
-                take<T, S, CL, Q8>(p, cur, 1, run, t0, dt);
+                take<T, S, CL, Q8>(p, from, 1, run, t0, dt);
                 if (p.z.p) {
-                    take<T, S, CL, Q8>(p, cur, 2, run, t0, z);
-                    take<T, S, CL, Q8>(p, cur, 3, run, t0, dy);
+                    take<T, S, CL, Q8>(p, from, 2, run, t0, z);
+                    take<T, S, CL, Q8>(p, from, 3, run, t0, dy);
                 }
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const int c = run.c(i), tl = run.t(i), o = c * H::RO + tl;
-                    const float4 s = st[c * (TT + 1) + tl];
-                    const float g = gs[c * (TT + 1) + tl].x;
-                    const float u = us[o], Dv = prm[c * 8 + 6];
+                    const float4 s = in.st[c * (TT + 1) + tl];
+                    const float g = in.gs[c * (TT + 1) + tl].x;
+                    const float u = in.us[o], Dv = prm[c * 8 + 6];
                     const float s1 = s1s[o], s2 = s2s[o] * kLn2;
                     du[i] = fmaf(g, Dv, s.x * s1);
                     const float ddelta = fmaf(u, s1, s2);
@@ -1156,19 +1117,243 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                     if (p.z.p && p.dz) put_run<T, E>(static_cast<T*>(p.dz) + at, rev, p.vec_out, hi, dz);
                 }
             }
+        };
+        if (p.async)                                           // a thread reads back its own entries
+            for (int k = hid; k < K::COUNT; k += H::NH) table[k] = K::make(p, b, d0, k);
+        fetch(0);
+        for (int n = -1; n < ntiles; ++n) {
+            cp_async_wait();
+            if (n > 0) finish(n - 1);
+            named_bar_sync(1, H::NH);                          // tile n + 1 is here, n - 1 finished
+            if (n + 2 < ntiles) fetch(n + 2);
+            if (n + 1 < ntiles) stage(n + 1);
+            __syncthreads();
+        }
+        finish(ntiles - 1);
+        if constexpr (!CL) {
+            // the threads of a channel are neighbours within a warp (TT / EPT of them)
+            constexpr int PER = TT / E;
+#pragma unroll
+            for (int w = 1; w < PER; w *= 2) {
+                dD += __shfl_xor_sync(0xffffffffu, dD, w);
+                dBias += __shfl_xor_sync(0xffffffffu, dBias, w);
+            }
+            if (hid % PER == 0 && d0 + run.ch < p.dim) {
+                float* o = p.pD + (row * p.dim + d0 + run.ch) * 2;
+                o[0] = dD;
+                o[1] = dBias;
+            }
+        } else {
+            named_bar_sync(1, H::NH);
+            for (int c = hid; c < H::G; c += H::NH) {
+                if (d0 + c >= p.dim) break;
+                float v0 = 0.f, v1 = 0.f;
+                for (int t = 0; t < TT; ++t) {
+                    v0 += sums[c * TT + t];
+                    v1 += sums[H::G * TT + c * TT + t];
+                }
+                float* o = p.pD + (row * p.dim + d0 + c) * 2;
+                o[0] = v0;
+                o[1] = v1;
+            }
+        }
+        return;
+    }
+
+    uint64_t m[KL][2], dA[KL][2], A2[KL][2];
+    // where a thread keeps them between its groups of channels
+    auto place = [&](int kc, int kl) { return carry + ((size_t)(kc * KL + kl) * 32 * H::W + tid) * 8; };
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+        for (int kl = 0; kl < KL; ++kl) {
+            const int d = d0 + H::channel(warp, kc, cl, j, kl);
+            dA[kl][0] = dA[kl][1] = 0;
+            m[kl][0] = m[kl][1] = 0;
+            if (te == L) load_state<S>(p, p.dhl, b, d, j, m[kl]);
+            else if (d < p.dim) ldpair(p.sumR + ns_off<S>(p, row, d, j), m[kl]);
+            if constexpr (REGS) {
+                load_A<S, HEADS>(p, d, j, A2[kl]);
+            } else {
+                stpair(place(kc, kl), m[kl]);
+                stpair(place(kc, kl) + 4, dA[kl]);
+            }
+        }
+    // the states before sub-tile `sub` of a tile, for group kc; fetched one use ahead
+    auto load_ckpt = [&](int tile, int sub, int kc, uint64_t (&v)[KL][2]) {
+#pragma unroll
+        for (int kl = 0; kl < KL; ++kl) {
+            const int d = d0 + H::channel(warp, kc, cl, j, kl);
+            if (d < p.dim)
+                ldpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + (tb + tile * TT) / ST + sub, d, j), v[kl]);
+        }
+    };
+    uint64_t hn[KL][2];
+#pragma unroll
+    for (int kl = 0; kl < KL; ++kl) hn[kl][0] = hn[kl][1] = 0;
+    load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
+    __syncthreads();                                           // tile 0 is staged
+    for (int n = 0; n < ntiles; ++n) {
+        const int tile = ntiles - 1 - n, t0 = tb + tile * TT;
+        const BwdStaged<S> in = staged.at(n & 1, kStaged);
+        const float4* st = in.st;
+        const float2* gs = in.gs;
+        const float *Bs = in.Bs, *Cs = in.Cs;
+        float* ys = outs + (n & 1) * 3 * H::kOut;
+        float *s1s = ys + H::kOut, *s2s = s1s + H::kOut;
+        const uint32_t starts = mask[n & 1];
+#pragma unroll 1
+        for (int sub = H::NSUB - 1; sub >= 0; --sub) {
+            constexpr int PT = 4 / H::NC;                      // dB, dC values left per step
+            float rB[ST * PT], rC[ST * PT];
+            if constexpr (KC > 1) {
+#pragma unroll
+                for (int i = 0; i < ST * PT; ++i) rB[i] = rC[i] = 0.f;
+            }
+#pragma unroll 1
+            for (int kc = 0; kc < KC; ++kc) {
+                const int sq = slot_order<S>(H::channel(warp, kc, cl, 0, 0));
+                uint64_t h0[KL][2];
+#pragma unroll
+                for (int kl = 0; kl < KL; ++kl) {
+                    h0[kl][0] = hn[kl][0];
+                    h0[kl][1] = hn[kl][1];
+                }
+                if (kc + 1 < KC) load_ckpt(tile, sub, kc + 1, hn);
+                else if (sub > 0) load_ckpt(tile, sub - 1, 0, hn);
+                else if (tile > 0) load_ckpt(tile - 1, H::NSUB - 1, 0, hn);
+                int so[KL];
+#pragma unroll
+                for (int kl = 0; kl < KL; ++kl) {
+                    const int c = H::channel(warp, kc, cl, j, kl);
+                    so[kl] = c * (TT + 1) + sub * ST;
+                    if constexpr (!REGS) {
+                        load_A<S, HEADS>(p, d0 + c, j, A2[kl]);
+                        ldpair(place(kc, kl), m[kl]);
+                        ldpair(place(kc, kl) + 4, dA[kl]);
+                    }
+                }
+                const float* Br = Bs + sq * H::RQ + sub * ST * H::RB + 4 * j;
+                const float* Cr = Cs + sq * H::RQ + sub * ST * H::RB + 4 * j;
+                uint64_t a[KL][ST][2], h[KL][ST][2];
+                {
+                    uint64_t du2[KL][ST];
+#pragma unroll
+                    for (int kl = 0; kl < KL; ++kl)
+                        decays<HEADS, ST>(A2[kl], st + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
+#pragma unroll
+                    for (int i = 0; i < ST; ++i) {
+                        uint64_t bv[2];
+                        ldpair(Br + i * H::RB, bv);
+#pragma unroll
+                        for (int kl = 0; kl < KL; ++kl)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                h[kl][i][k] = fma2(a[kl][i][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k],
+                                                   mul2(du2[kl][i], bv[k]));
+                    }
+                }
+                float y[8], s1[8], s2[8];
+#pragma unroll
+                for (int i = ST - 1; i >= 0; --i) {
+                    uint64_t bv[2], cv[2], tb2[2], tc2[2];
+                    ldpair(Br + i * H::RB, bv);
+                    ldpair(Cr + i * H::RB, cv);
+#pragma unroll
+                    for (int kl = 0; kl < KL; ++kl) {
+                        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(st + so[kl] + i);
+                        const uint64_t g2 = *reinterpret_cast<const uint64_t*>(gs + so[kl] + i);
+                        uint64_t lam[2], q[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            lam[k] = fma2(g2, cv[k], m[kl][k]);
+                            m[kl][k] = mul2(a[kl][i][k], lam[k]);
+                            q[k] = mul2(m[kl][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k]);
+                            dA[kl][k] = fma2(q[k], s.x, dA[kl][k]);
+                            tb2[k] = kl ? fma2(lam[k], s.y, tb2[k]) : mul2(lam[k], s.y);
+                            tc2[k] = kl ? fma2(g2, h[kl][i][k], tc2[k]) : mul2(g2, h[kl][i][k]);
+                        }
+                        const int v = kl * ST + i;
+                        const float2 fy = upk2(fma2(cv[1], h[kl][i][1], mul2(cv[0], h[kl][i][0])));
+                        const float2 f1 = upk2(fma2(bv[1], lam[1], mul2(bv[0], lam[0])));
+                        y[v] = fy.x + fy.y;
+                        s1[v] = f1.x + f1.y;
+                        if constexpr (HEADS) {
+                            const float2 f2 = upk2(add2(q[0], q[1]));
+                            s2[v] = lo2(A2[kl][0]) * (f2.x + f2.y);
+                        } else {
+                            const float2 f2 = upk2(fma2(q[1], A2[kl][1], mul2(q[0], A2[kl][0])));
+                            s2[v] = f2.x + f2.y;
+                        }
+                    }
+                    float vb[PT], vc[PT];
+                    reduce_slots<S>(tb2, vb);
+                    reduce_slots<S>(tc2, vc);
+#pragma unroll
+                    for (int k = 0; k < PT; ++k) {
+                        rB[i * PT + k] = KC > 1 ? rB[i * PT + k] + vb[k] : vb[k];
+                        rC[i * PT + k] = KC > 1 ? rC[i * PT + k] + vc[k] : vc[k];
+                    }
+                }
+                using Sums = StateSums<S>;
+                Sums::sum(y, lane);
+                Sums::sum(s1, lane);
+                Sums::sum(s2, lane);
+                constexpr int SPAN = Sums::kTrade ? 2 * (ST / Sums::kept()) : ST / Sums::kept();
+                if (j < SPAN) {                                // lanes beyond hold the same sums
+                    const int c = H::channel(warp, kc, cl, j, 0);
+                    const int o = c * H::RO + sub * ST + Sums::first(lane);
+#pragma unroll
+                    for (int k = 0; k < Sums::kept(); ++k) {
+                        ys[o + k] = y[k];
+                        s1s[o + k] = s1[k];
+                        s2s[o + k] = s2[k];
+                    }
+                }
+                if constexpr (!REGS) {
+#pragma unroll
+                    for (int kl = 0; kl < KL; ++kl) {
+                        stpair(place(kc, kl), m[kl]);
+                        stpair(place(kc, kl) + 4, dA[kl]);
+                    }
+                }
+            }
+            const int sq = slot_order<S>(H::channel(0, 0, cl, 0, 0));
+            if constexpr (PT == 1) {
+                using Sums = GroupSums<S>;
+                Sums::sum(rB, lane);
+                Sums::sum(rC, lane);
+                const int first = Sums::first(lane);
+#pragma unroll
+                for (int k = 0; k < Sums::kept(); ++k) {
+                    float* o = part + (warp * TT + sub * ST + first + k) * H::RP + 4 * j + sq;
+                    o[0] = rB[k];
+                    o[H::NS] = rC[k];
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < ST * PT; ++k) {            // slot k % PT * NC of step k / PT
+                    float* o = part + (warp * TT + sub * ST + k / PT) * H::RP + 4 * j +
+                               (k % PT * H::NC ^ sq);
+                    o[0] = rB[k];
+                    o[H::NS] = rC[k];
+                }
+            }
         }
         // the CTA's dB and dC of the tile
+        if (H::W > 1) named_bar_sync(2, 32 * H::W);
         {
             constexpr int ROW = 2 * H::NS;
             float* out = p.parts + (((int64_t)blockIdx.x * p.batch + b) * L + t0) * ROW;
             const int n = min(TT, te - t0) * ROW;
 #pragma unroll
-            for (int k = tid * 4; k < TT * ROW; k += kBwdThreads * 4) {
+            for (int k = tid * 4; k < TT * ROW; k += 32 * H::W * 4) {
                 if (k >= n) break;
-                float4 v = *reinterpret_cast<const float4*>(part + k);
+                const float* from = part + k / ROW * H::RP + k % ROW;
+                float4 v = *reinterpret_cast<const float4*>(from);
 #pragma unroll
-                for (int w = 1; w < kBwdWarps; ++w) {
-                    const float4 q = *reinterpret_cast<const float4*>(part + w * TT * ROW + k);
+                for (int w = 1; w < H::W; ++w) {
+                    const float4 q = *reinterpret_cast<const float4*>(from + w * TT * H::RP);
                     v.x += q.x;
                     v.y += q.y;
                     v.z += q.z;
@@ -1177,27 +1362,22 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                 *reinterpret_cast<float4*>(out + k) = v;
             }
         }
+        __syncthreads();                                       // tile n is done, n + 1 staged
     }
     // what the sweep summed over its steps
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc) {
-        const int d = d0 + (warp * KC + kc) * H::CW + cl;
-        const int r = REGS ? kc : 0;
-        if constexpr (!REGS) {
-            ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8, m[0]);
-            ldpair(carry + ((size_t)kc * kBwdThreads + tid) * 8 + 4, dA[0]);
-        }
-        if constexpr (HEADS) {                                 // (rows, dim): summed over the states
-            const float2 f = upk2(add2(dA[r][0], dA[r][1]));
-            float v = f.x + f.y;
 #pragma unroll
-            for (int w = 1; w < S; w *= 2) v += __shfl_xor_sync(0xffffffffu, v, w);
-            if (j == 0 && d < p.dim) p.pA[row * p.dim + d] = v;
-        }
-        if (d < p.dim) {
-            if constexpr (!HEADS) stpair(p.pA + ns_off<S>(p, row, d, j), dA[r]);
+        for (int kl = 0; kl < KL; ++kl) {
+            const int d = d0 + H::channel(warp, kc, cl, j, kl);
+            if constexpr (!REGS) {
+                ldpair(place(kc, kl), m[kl]);
+                ldpair(place(kc, kl) + 4, dA[kl]);
+            }
+            if (d >= p.dim) continue;
+            if constexpr (!HEADS) stpair(p.pA + ns_off<S>(p, row, d, j), dA[kl]);
             if (seg == 0 && p.dh0) {
-                const float2 lo = upk2(m[r][0]), hi = upk2(m[r][1]);
+                const float2 lo = upk2(m[kl][0]), hi = upk2(m[kl][1]);
                 const float f[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -1206,32 +1386,19 @@ __global__ void __launch_bounds__(kBwdThreads, S <= 4 ? 3 : 2) scan_bwd_kernel(c
                 }
             }
         }
-    }
-    __syncthreads();
-    if constexpr (!CL) {
-        // the threads of a channel are neighbours within a warp (TT / EPT of them)
-        constexpr int PER = TT / E;
+        if constexpr (HEADS) {                                 // (rows, dim): summed over the states
+            constexpr bool kTrade = StateSums<S>::kTrade;
+            float v[KL];
 #pragma unroll
-        for (int w = 1; w < PER; w *= 2) {
-            dD += __shfl_xor_sync(0xffffffffu, dD, w);
-            dBias += __shfl_xor_sync(0xffffffffu, dBias, w);
-        }
-        if (tid % PER == 0 && d0 + run.ch < p.dim) {
-            float* o = p.pD + (row * p.dim + d0 + run.ch) * 2;
-            o[0] = dD;
-            o[1] = dBias;
-        }
-    } else {
-        for (int c = tid; c < H::G; c += kBwdThreads) {
-            if (d0 + c >= p.dim) break;
-            float v0 = 0.f, v1 = 0.f;
-            for (int t = 0; t < TT; ++t) {
-                v0 += sums[c * TT + t];
-                v1 += sums[H::G * TT + c * TT + t];
+            for (int kl = 0; kl < KL; ++kl) {
+                const float2 f = upk2(add2(dA[kl][0], dA[kl][1]));
+                v[kl] = f.x + f.y;
             }
-            float* o = p.pD + (row * p.dim + d0 + c) * 2;
-            o[0] = v0;
-            o[1] = v1;
+            if constexpr (kTrade) v[0] += __shfl_xor_sync(0xffffffffu, v[KL - 1], 1);
+#pragma unroll
+            for (int w = kTrade ? 2 : 1; w < S; w *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+            const int d = d0 + H::channel(warp, kc, cl, j, 0);
+            if (j < (kTrade ? 2 : 1) && d < p.dim) p.pA[row * p.dim + d] = v[0];
         }
     }
 }

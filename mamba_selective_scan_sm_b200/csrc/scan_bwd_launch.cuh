@@ -8,33 +8,33 @@
 namespace ssm {
 
 template <typename K>
-inline cudaError_t launch_with_smem(K k, dim3 grid, int smem, const BwdParams& p, cudaStream_t st) {
+inline cudaError_t launch_with_smem(K k, dim3 grid, int threads, int smem, const BwdParams& p, cudaStream_t st) {
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    k<<<grid, kBwdThreads, smem, st>>>(p);
+    k<<<grid, threads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
 inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t st) {
     using H = BwdShape<S>;
-    constexpr int kRaw = 2 * BwdRaw<T, S, CL>::BYTES;
+    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES, kHead = (H::kPrm + H::kMask) * 4;
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
-        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid,
-                                (H::kSt + H::kBC + H::kPrm + H::kMask) * 4 + kRaw + BwdCopies<T, S, CL, Q8, false>::COUNT * 16,
+        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid, H::NT,
+                                2 * H::kStaged(false) * 4 + kHead + 2 * kRaw +
+                                    BwdCopies<T, S, CL, Q8, false>::COUNT * 16,
                                 p, st);
     if (what == 1)
-        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kSummary>, grid,
-                                (H::kSt + H::kG + H::kU + 2 * H::kBC + H::kPrm + H::kMask) * 4 + kRaw +
+        return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kSummary>, grid, H::NT,
+                                2 * H::kStaged(true) * 4 + kHead + 2 * kRaw +
                                     BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                                 p, st);
-    return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid,
-                            (H::kSt + H::kG + H::kU + 3 * H::kOut + 2 * H::kBC + H::kPart + H::kPrm +
-                             H::kMask + H::kCarry + (CL ? H::kSum : 0)) * 4 + kRaw +
-                                BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
+    return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid, H::NT,
+                            (2 * H::kStaged(true) + 6 * H::kOut + H::kPart + H::kCarry + (CL ? H::kSum : 0)) * 4 +
+                                kHead + 3 * kRaw + BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                             p, st);
 }
 

@@ -84,13 +84,29 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     pl->v = scan_bwd_variant(pl->lanes);
     const int64_t tile = pl->v.tile, ntiles = std::max<int64_t>(1, (L + tile - 1) / tile);
     pl->groups = (int)((D + pl->v.channels - 1) / pl->v.channels);
-    // Segments. One sweep per row takes two exps per (channel, step, state), segments three,
-    // so a grid that fills half of the SMs' CTA slots (two CTAs of 4 warps per SM) is left
-    // alone, and a smaller one is split until it fills them, down to one tile a segment.
+    // Segments. One sweep per row takes two exps per (channel, step, state), segments a third
+    // and one more pass over the inputs (about 1.3 times the time where one sweep per row fills
+    // the GPU): so a grid that fills three quarters of the SMs' CTA slots is left alone. A
+    // smaller one is split so that its waves of CTAs, each as long as a segment, take the least
+    // time together, up to some four waves (measured: B8 D1536 L2048 1.10 ms in one sweep, 1.32
+    // in 9 segments; B4 D1536 L2048 1.15 in one, 0.90 in 9; B1 D5120 L16384 6.45 in one, 3.6
+    // in 9 to 27; d_state 128 with A per head, B2 D1536 L2048, 2.51 in one, 1.99 in 3).
     int64_t nseg = a->num_segments;
     if (nseg == 0) {
-        const int64_t ctas = pl->groups * Bn, slots = 2 * kNumSMs;
-        nseg = ctas > 0 && 2 * ctas <= slots ? slots / ctas : 1;
+        const int64_t ctas = pl->groups * Bn, slots = (int64_t)kNumSMs * pl->v.ctas;
+        nseg = 1;
+        if (ctas > 0 && 4 * ctas < 3 * slots) {
+            double best = 1e30;
+            const int64_t most = std::min<int64_t>(ntiles, 4 * slots / ctas);
+            for (int64_t n = 1; n <= most; ++n) {
+                const double waves = (double)((ctas * n + slots - 1) / slots);
+                const double t = waves / n + 0.002 * n + (n > 1 ? 0.1 * waves / n : 0.0);
+                if (t < best) {
+                    best = t;
+                    nseg = n;
+                }
+            }
+        }
     }
     nseg = std::max<int64_t>(1, std::min<int64_t>({nseg, ntiles, 4096}));
     const int64_t per = (ntiles + nseg - 1) / nseg;
@@ -357,9 +373,10 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         c.part = f(pl.conv_part);
         c.chunks = pl.conv_chunks;
         c.chunk_len = conv_bwd_chunk(cl);
-        // runs of 8 positions, or channel-last of 4 channels (4 codes, 8 or 16 bytes)
+        // runs of 16 positions (8-bit: from multiples of 16, so each within one block), or
+        // channel-last of 4 channels
         c.vec = is_aligned(a->u, 16) && is_aligned(a->du, 16) &&
-                (cl ? (p.x.s.p % 4 == 0 && c.sdx.p % 4 == 0 && D % 4 == 0) : (L % 8 == 0 && !packed8));
+                (cl ? (p.x.s.p % 4 == 0 && c.sdx.p % 4 == 0 && D % 4 == 0) : (L % (packed8 ? 16 : 8) == 0));
         if ((e = launch_conv_bwd((int)es, cl, c, s)) != cudaSuccess)
             return api_cuda(e, "conv gradient launch");
         ConvReduceParams cr{(int)D, a->conv_width, Bn * pl.conv_chunks, c.part,

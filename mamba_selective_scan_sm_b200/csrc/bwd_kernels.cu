@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdRed
 
 template <int S> static BwdVariant variant_of() {
     using H = BwdShape<S>;
-    return {H::NS, H::G, H::TT, H::T, H::KL - 1, H::NC - 1};
+    return {H::NS, H::G, H::TT, H::T, H::CTAS, H::KL - 1, H::NC - 1};
 }
 BwdVariant scan_bwd_variant(int lanes) {
     return lanes == 1   ? variant_of<1>()
@@ -169,8 +169,14 @@ cudaError_t launch_conv_bwd(int elem_size, bool channel_last, const ConvBwdParam
     } else {
         const int64_t rows = (int64_t)p.batch * p.dim;
         const dim3 g(p.chunks, (unsigned)(rows < 65535 ? rows : 65535), (unsigned)((rows + 65534) / 65535));
-        if (elem_size == 2) conv_bwd_row_kernel<__nv_bfloat16><<<g, kConvRowThreads, 0, st>>>(p);
-        else conv_bwd_row_kernel<float><<<g, kConvRowThreads, 0, st>>>(p);
+        const bool q8 = p.x.scale != nullptr;
+        if (elem_size == 2) {
+            if (q8) conv_bwd_row_kernel<__nv_bfloat16, true><<<g, kConvRowThreads, 0, st>>>(p);
+            else conv_bwd_row_kernel<__nv_bfloat16, false><<<g, kConvRowThreads, 0, st>>>(p);
+        } else {
+            if (q8) conv_bwd_row_kernel<float, true><<<g, kConvRowThreads, 0, st>>>(p);
+            else conv_bwd_row_kernel<float, false><<<g, kConvRowThreads, 0, st>>>(p);
+        }
     }
     return cudaGetLastError();
 }

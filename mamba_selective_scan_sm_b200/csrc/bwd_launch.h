@@ -11,6 +11,7 @@ namespace ssm {
 struct BwdVariant {
     int ns, channels, tile;
     int steps;                    // between two checkpoints of the state
+    int ctas;                     // of the backward sweep per SM
     int order_shift, order_mask;  // scratch states of channel d stand at n ^ (d >> shift & mask)
 };
 BwdVariant scan_bwd_variant(int lanes);

@@ -13,7 +13,7 @@
 
 namespace ssm {
 
-constexpr int kConvRun = 8;                                    // steps per thread along a row
+constexpr int kConvRun = 16;                                   // steps per thread along a row
 constexpr int kConvRowThreads = 128;
 constexpr int kConvRowChunk = kConvRun * kConvRowThreads;      // steps per CTA along a row
 constexpr int kConvClChunk = 64;                               // steps per thread, channel-last
@@ -41,9 +41,10 @@ __device__ __forceinline__ void take_dense(const T* p, bool rev, float (&f)[R]) 
     take_run<T, R>(rev ? p - (R - 1) : p, rev, f);
 }
 
-template <typename T>
+template <typename T, bool Q8>
 __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const ConvBwdParams p) {
     constexpr int R = kConvRun;
+    using X = std::conditional_t<Q8, int8_t, T>;
     const int L = p.seqlen, dir = p.reverse ? -1 : 1;
     const int64_t rowid = (int64_t)blockIdx.z * 65535 + blockIdx.y;
     if (rowid >= (int64_t)p.batch * p.dim) return;
@@ -60,16 +61,25 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
         float x[R + 6], dp[R + 3];
         const bool rev = p.reverse;
         const int pos0 = rev ? L - 1 - t0 : t0;
-        const T* xr = static_cast<const T*>(p.x.p) + (int64_t)b * p.x.s.b + (int64_t)d * p.x.s.c;
+        const X* xr = static_cast<const X*>(p.x.p) + (int64_t)b * p.x.s.b + (int64_t)d * p.x.s.c;
+        // codes to values: n of them from position ps on in the run's direction, of one block
+        auto scaled = [&](float* v, int n, int ps) {
+            if constexpr (Q8) {
+                const float sc = p.x.scale[(int64_t)b * p.x.ss.b + (int64_t)d * p.x.ss.c + ps / kBlock8];
+                for (int i = 0; i < n; ++i) v[i] *= sc;
+            }
+        };
         const int64_t orow = (int64_t)b * p.sdo.b + (int64_t)d * p.sdo.c;
-        if (p.vec) {
-            // whole rows of aligned runs: the run, 4 steps behind it and 4 before it
+        if (p.vec && t0 + R <= L) {
+            // a whole run of an aligned row: the run, 4 steps before it and 4 behind it
             float run[R], near[4];
-            take_dense<T, R>(xr + pos0, rev, run);
+            take_dense<X, R>(xr + pos0, rev, run);
+            scaled(run, R, pos0);
 #pragma unroll
             for (int i = 0; i < R; ++i) x[3 + i] = run[i];
             if (t0 > 0) {
-                take_dense<T, 4>(xr + pos0 - dir * 4, rev, near);
+                take_dense<X, 4>(xr + pos0 - dir * 4, rev, near);
+                scaled(near, 4, pos0 - dir * 4);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) x[i] = near[i + 1];
             } else {
@@ -79,7 +89,10 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
             const bool more = t0 + R < L;
 #pragma unroll
             for (int i = 0; i < 4; ++i) near[i] = 0.f;
-            if (more) take_dense<T, 4>(xr + pos0 + dir * R, rev, near);
+            if (more) {
+                take_dense<X, 4>(xr + pos0 + dir * R, rev, near);
+                scaled(near, 4, pos0 + dir * R);
+            }
 #pragma unroll
             for (int i = 0; i < 3; ++i) x[R + 3 + i] = near[i];
 #pragma unroll
@@ -150,19 +163,17 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
                     static_cast<T*>(p.dhist)[rowid * (p.width - 1) + (p.width - 4 + m)] =
                         Elem<T>::from_f(dx[m]);
     }
-    __shared__ float red[kConvRowThreads / 32][5];
+    __shared__ __align__(16) float red[5][kConvRowThreads];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) {
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) sw[k] += __shfl_xor_sync(0xffffffffu, sw[k], o);
-        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32][k] = sw[k];
-    }
+    for (int k = 0; k < 5; ++k) red[k][threadIdx.x] = sw[k];
     __syncthreads();
-    if (threadIdx.x < 5) {
-        float v = 0.f;
+    static_assert(kConvRowThreads == 128, "a warp's lanes take 4 threads' sums each");
+    for (int k = threadIdx.x / 32; k < 5; k += kConvRowThreads / 32) {
+        const float4 q = reinterpret_cast<const float4*>(red[k])[threadIdx.x % 32];
+        float v = (q.x + q.y) + (q.z + q.w);
 #pragma unroll
-        for (int i = 0; i < kConvRowThreads / 32; ++i) v += red[i][threadIdx.x];
-        p.part[(((int64_t)b * p.chunks + blockIdx.x) * p.dim + d) * 5 + threadIdx.x] = v;
+        for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (threadIdx.x % 32 == 0) p.part[(((int64_t)b * p.chunks + blockIdx.x) * p.dim + d) * 5 + k] = v;
     }
 }
 
@@ -246,33 +257,39 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
             if (t >= te + 3) break;
             if (t < L) scaled(t, x[k]);
             float out[E];
+            auto step = [&](auto within) {                     // all 4 taps lie within the sequence
+                constexpr bool all = decltype(within)::value;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                xw[3][i] = xw[2][i];
-                xw[2][i] = xw[1][i];
-                xw[1][i] = xw[0][i];
-                xw[0][i] = x[k][i];
-                acc[3][i] = acc[2][i];                         // acc[lag]: dx_{t-lag} so far
-                acc[2][i] = acc[1][i];
-                acc[1][i] = acc[0][i];
-                acc[0][i] = 0.f;
-                float g = dp[k][i];
-                if (p.silu) {
-                    float pre = bias[i];
+                for (int i = 0; i < E; ++i) {
+                    xw[3][i] = xw[2][i];
+                    xw[2][i] = xw[1][i];
+                    xw[1][i] = xw[0][i];
+                    xw[0][i] = x[k][i];
+                    acc[3][i] = acc[2][i];                     // acc[lag]: dx_{t-lag} so far
+                    acc[2][i] = acc[1][i];
+                    acc[1][i] = acc[0][i];
+                    acc[0][i] = 0.f;
+                    float g = dp[k][i];
+                    if (p.silu) {
+                        float pre = bias[i];
+#pragma unroll
+                        for (int lag = 0; lag < 4; ++lag)
+                            if (all || lag <= sn[k]) pre = fmaf(w[lag][i], xw[lag][i], pre);
+                        g *= dsilu(pre);
+                    }
 #pragma unroll
                     for (int lag = 0; lag < 4; ++lag)
-                        if (lag <= sn[k]) pre = fmaf(w[lag][i], xw[lag][i], pre);
-                    g *= dsilu(pre);
-                }
+                        if (all || lag <= sn[k]) acc[lag][i] = fmaf(w[lag][i], g, acc[lag][i]);
+                    const float gs = t < te ? g : 0.f;         // the halo's steps are another chunk's
 #pragma unroll
-                for (int lag = 0; lag < 4; ++lag)
-                    if (lag <= sn[k]) {
-                        acc[lag][i] = fmaf(w[lag][i], g, acc[lag][i]);
-                        if (t < te) sw[lag][i] = fmaf(g, xw[lag][i], sw[lag][i]);
-                    }
-                if (t < te) sw[4][i] += g;
-                out[i] = acc[3][i];
-            }
+                    for (int lag = 0; lag < 4; ++lag)
+                        if (all || lag <= sn[k]) sw[lag][i] = fmaf(gs, xw[lag][i], sw[lag][i]);
+                    sw[4][i] += gs;
+                    out[i] = acc[3][i];
+                }
+            };
+            if (sn[k] >= 3) step(std::true_type{});
+            else step(std::false_type{});
             const int s = t - 3;                               // dx_s is complete
             if (s >= tb) {
                 put_run<T, E>(static_cast<T*>(p.dx) + (int64_t)b * p.sdx.b + d + (int64_t)pos(s) * p.sdx.p,

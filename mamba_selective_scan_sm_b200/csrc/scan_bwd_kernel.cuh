@@ -48,6 +48,7 @@ template <int S> struct BwdShape {
     static constexpr int W = S == 4 ? 2 : 4;                   // scan warps per CTA
     static constexpr int NH = S == 1 || S == 2 ? 128 : 64;     // helper threads
     static constexpr int NT = 32 * W + NH;
+    static constexpr int CTAS = S == 4 ? 3 : S == 8 ? 2 : 1;   // per SM, by registers and shared memory
     static constexpr int KC = S <= 8 ? 1 : S / 8;              // such groups a warp takes in turn
     static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
     static constexpr int G = W * CW * KL * KC;                 // channels per CTA
@@ -57,8 +58,8 @@ template <int S> struct BwdShape {
     static constexpr int RB = NS;                              // row of B / C in floats
     // shared memory, in floats
     // one of two staged tiles
-    static constexpr int kSt = 4 * G * (TT + 1);               // {delta, delta, delta u, delta u}
-    static constexpr int kG = 2 * G * (TT + 1);                // {g, g}
+    static constexpr int kSt = 2 * G * (TT + 1);               // {delta, delta u}
+    static constexpr int kG = G * (TT + 1);
     static constexpr int RO = TT + 1;                          // row of u, y, s1, s2 in floats
     static constexpr int kU = G * RO;
     static constexpr int kOut = G * RO;                        // one of y, s1, s2
@@ -620,13 +621,13 @@ __device__ __forceinline__ void each_pair(float (&out)[E], const float (&in)[E],
     }
 }
 
-// Turn a tile's raw inputs into what the recurrences take: delta and delta u (each twice, as
-// the pairs they take) per channel and step, g and u where ADJ, and the rows of B (and C
+// Turn a tile's raw inputs into what the recurrences take: delta and delta u per channel and
+// step, g and u where ADJ, and the rows of B (and C
 // where ADJ) in each order of the states. Steps past the end and channels past dim get
 // zeros: a = 1 and no input, which leave both recurrences where they are.
 template <typename T, int S, bool CL, bool Q8, bool ADJ>
 __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, int d0, int t0, const uint8_t* raw,
-                                           const float* prm, float4* st, float2* gs, float* us,
+                                           const float* prm, float2* st, float* gs, float* us,
                                            float* Bs, float* Cs, uint32_t* mask) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
@@ -733,9 +734,9 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
         }
         const int o = r.c(i) * (H::TT + 1) + r.t(i);
         const float du = dl * u[i];
-        st[o] = make_float4(dl, dl, du, du);
+        st[o] = make_float2(dl, du);
         if constexpr (ADJ) {
-            gs[o] = make_float2(g[i], g[i]);
+            gs[o] = g[i];
             us[r.c(i) * H::RO + r.t(i)] = u[i];
         }
     }
@@ -797,13 +798,13 @@ __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint
 
 // Decays and delta u of the T steps from row, the decays zero at the sequence starts in mask.
 template <bool HEADS, int T>
-__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float4* row, uint32_t mask,
+__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, uint32_t mask,
                                        uint64_t (&a)[T][2], uint64_t (&du2)[T]) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(row + i);
-        decay<HEADS>(A2, s.x, a[i]);
-        du2[i] = s.y;
+        const float2 s = row[i];
+        decay<HEADS>(A2, pk2(s.x, s.x), a[i]);
+        du2[i] = pk2(s.y, s.y);
     }
     if (mask) {
 #pragma unroll
@@ -844,20 +845,19 @@ __device__ __forceinline__ int64_t ns_off(const BwdParams& p, int64_t row, int d
 // The arrays of a staged tile (one of two).
 template <int S> struct BwdStaged {
     using H = BwdShape<S>;
-    float4* st;
-    float2* gs;
-    float *us, *Bs, *Cs;
+    float2* st;
+    float *gs, *us, *Bs, *Cs;
     __device__ __forceinline__ BwdStaged(float* sm, bool adj) {
-        st = reinterpret_cast<float4*>(sm);
-        gs = reinterpret_cast<float2*>(sm + H::kSt);
+        st = reinterpret_cast<float2*>(sm);
+        gs = sm + H::kSt;
         us = sm + H::kSt + (adj ? H::kG : 0);
         Bs = us + (adj ? H::kU : 0);
         Cs = Bs + H::kBC;
     }
     __device__ __forceinline__ BwdStaged at(int n, int size) const {
         BwdStaged r = *this;
-        r.st += n * size / 4;
-        r.gs += n * size / 2;
+        r.st += n * size / 2;
+        r.gs += n * size;
         r.us += n * size;
         r.Bs += n * size;
         r.Cs += n * size;
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
 #pragma unroll
                     for (int kl = 0; kl < KL; ++kl) {
                         uint64_t g2 = 0;
-                        if (SUM) g2 = *reinterpret_cast<const uint64_t*>(in.gs + so[kl] + i);
+                        if (SUM) g2 = pk2(in.gs[so[kl] + i], in.gs[so[kl] + i]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             h[kc][kl][k] = fma2(a[kl][i][k], h[kc][kl][k], mul2(du2[kl][i], bv[k]));
@@ -990,31 +990,51 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
 // the adjoint carry a_t lam_t from behind it. One thread per (batch row, channel, state).
 template <int S>
 __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) {
-    constexpr int NS = 4 * S;
+    constexpr int NS = 4 * S, U = 8;                           // U segments' loads together
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int64_t per = (int64_t)p.batch * p.dim * NS;
     if (idx >= per) return;
-    const int64_t bd = idx / NS;
-    const int n = (int)(idx % NS) ^ slot_order<S>((int)(bd % p.dim));
-    float h = p.h0 && n < p.dstate ? p.h0[bd * p.dstate + n] : 0.f;
-    float m = p.dhl && n < p.dstate ? p.dhl[bd * p.dstate + n] : 0.f;
-    for (int s = 0; s < p.nseg; ++s) {
-        const int64_t o = s * per + idx;
-        const float pr = p.sumP[o], e = p.sumS[o];
-        p.sumS[o] = h;
-        h = fmaf(pr, h, e);
+    const uint32_t bd = (uint32_t)(idx / NS);                  // batch * dim is below 2^31
+    const int n = (int)(idx % NS) ^ slot_order<S>((int)(bd % (uint32_t)p.dim));
+    float h = p.h0 && n < p.dstate ? p.h0[(int64_t)bd * p.dstate + n] : 0.f;
+    float m = p.dhl && n < p.dstate ? p.dhl[(int64_t)bd * p.dstate + n] : 0.f;
+    const float* P = p.sumP + idx;
+    float *Sx = p.sumS + idx, *Rx = p.sumR + idx;
+    for (int s0 = 0; s0 < p.nseg; s0 += U) {
+        float pr[U], e[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 + k < p.nseg) {
+                pr[k] = P[(s0 + k) * per];
+                e[k] = Sx[(s0 + k) * per];
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 + k < p.nseg) {
+                Sx[(s0 + k) * per] = h;
+                h = fmaf(pr[k], h, e[k]);
+            }
     }
-    for (int s = p.nseg - 1; s >= 0; --s) {
-        const int64_t o = s * per + idx;
-        const float pr = p.sumP[o], r = p.sumR[o];
-        p.sumR[o] = m;
-        m = fmaf(pr, m, r);
+    for (int s0 = p.nseg - 1; s0 >= 0; s0 -= U) {
+        float pr[U], r[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 - k >= 0) {
+                pr[k] = P[(s0 - k) * per];
+                r[k] = Rx[(s0 - k) * per];
+            }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 - k >= 0) {
+                Rx[(s0 - k) * per] = m;
+                m = fmaf(pr[k], m, r[k]);
+            }
     }
 }
 
 // The backward sweep.
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
-__global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) scan_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr int KC = H::KC, KL = H::KL, ST = H::T, TT = H::TT, E = H::EPT;
     constexpr bool REGS = KC == 1;                             // m and dA in registers, else carried over
@@ -1079,8 +1099,8 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) 
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const int c = run.c(i), tl = run.t(i), o = c * H::RO + tl;
-                    const float4 s = in.st[c * (TT + 1) + tl];
-                    const float g = in.gs[c * (TT + 1) + tl].x;
+                    const float2 s = in.st[c * (TT + 1) + tl];
+                    const float g = in.gs[c * (TT + 1) + tl];
                     const float u = in.us[o], Dv = prm[c * 8 + 6];
                     const float s1 = s1s[o], s2 = s2s[o] * kLn2;
                     du[i] = fmaf(g, Dv, s.x * s1);
@@ -1179,25 +1199,28 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) 
                 stpair(place(kc, kl) + 4, dA[kl]);
             }
         }
-    // the states before sub-tile `sub` of a tile, for group kc; fetched one use ahead
-    auto load_ckpt = [&](int tile, int sub, int kc, uint64_t (&v)[KL][2]) {
+    // The states before the next sub-tile to come (from the segment's last one backwards), for
+    // group kc: fetched one use ahead.
+    const float* ck = p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + (tb + (ntiles - 1) * TT) / ST + H::NSUB - 1, d0, j);
+    const int64_t ck_step = (int64_t)p.dim * H::NS;
+    uint64_t hn[KL][2];
+    auto load_ckpt = [&](int kc) {
 #pragma unroll
         for (int kl = 0; kl < KL; ++kl) {
-            const int d = d0 + H::channel(warp, kc, cl, j, kl);
-            if (d < p.dim)
-                ldpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + (tb + tile * TT) / ST + sub, d, j), v[kl]);
+            const int c = H::channel(warp, kc, cl, j, kl);
+            if (d0 + c < p.dim) ldpair(ck + c * H::NS, hn[kl]);
         }
     };
-    uint64_t hn[KL][2];
 #pragma unroll
     for (int kl = 0; kl < KL; ++kl) hn[kl][0] = hn[kl][1] = 0;
-    load_ckpt(ntiles - 1, H::NSUB - 1, 0, hn);
+    load_ckpt(0);
+    int left = ntiles * H::NSUB;                               // sub-tiles to come
     __syncthreads();                                           // tile 0 is staged
     for (int n = 0; n < ntiles; ++n) {
         const int tile = ntiles - 1 - n, t0 = tb + tile * TT;
         const BwdStaged<S> in = staged.at(n & 1, kStaged);
-        const float4* st = in.st;
-        const float2* gs = in.gs;
+        const float2* st = in.st;
+        const float* gs = in.gs;
         const float *Bs = in.Bs, *Cs = in.Cs;
         float* ys = outs + (n & 1) * 3 * H::kOut;
         float *s1s = ys + H::kOut, *s2s = s1s + H::kOut;
@@ -1219,9 +1242,12 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) 
                     h0[kl][0] = hn[kl][0];
                     h0[kl][1] = hn[kl][1];
                 }
-                if (kc + 1 < KC) load_ckpt(tile, sub, kc + 1, hn);
-                else if (sub > 0) load_ckpt(tile, sub - 1, 0, hn);
-                else if (tile > 0) load_ckpt(tile - 1, H::NSUB - 1, 0, hn);
+                if (kc + 1 < KC) {
+                    load_ckpt(kc + 1);
+                } else if (--left > 0) {
+                    ck -= ck_step;
+                    load_ckpt(0);
+                }
                 int so[KL];
 #pragma unroll
                 for (int kl = 0; kl < KL; ++kl) {
@@ -1261,16 +1287,17 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, S == 4 ? 3 : S == 8 ? 2 : 1) 
                     ldpair(Cr + i * H::RB, cv);
 #pragma unroll
                     for (int kl = 0; kl < KL; ++kl) {
-                        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(st + so[kl] + i);
-                        const uint64_t g2 = *reinterpret_cast<const uint64_t*>(gs + so[kl] + i);
+                        const float2 s = st[so[kl] + i];
+                        const float g = gs[so[kl] + i];
+                        const uint64_t d2 = pk2(s.x, s.x), du2 = pk2(s.y, s.y), g2 = pk2(g, g);
                         uint64_t lam[2], q[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             lam[k] = fma2(g2, cv[k], m[kl][k]);
                             m[kl][k] = mul2(a[kl][i][k], lam[k]);
                             q[k] = mul2(m[kl][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k]);
-                            dA[kl][k] = fma2(q[k], s.x, dA[kl][k]);
-                            tb2[k] = kl ? fma2(lam[k], s.y, tb2[k]) : mul2(lam[k], s.y);
+                            dA[kl][k] = fma2(q[k], d2, dA[kl][k]);
+                            tb2[k] = kl ? fma2(lam[k], du2, tb2[k]) : mul2(lam[k], du2);
                             tc2[k] = kl ? fma2(g2, h[kl][i][k], tc2[k]) : mul2(g2, h[kl][i][k]);
                         }
                         const int v = kl * ST + i;

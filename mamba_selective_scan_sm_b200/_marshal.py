@@ -2,8 +2,6 @@
 checked here (ValueError / TypeError), sizes and pointers in the library (SSMError)."""
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _abi
@@ -27,28 +25,28 @@ class Call:
 
     def ptr(self, t, name, shape, dtype):
         """A contiguous tensor's pointer (None for None or an empty one)."""
-        self.check(t, name, shape, dtype)
         if t is None:
             return None
+        self.check(t, name, shape, dtype)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr() or None
 
     def check(self, t, name, shape, dtype):
-        if t is None:
-            return
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, not on {self.device}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
     def strided(self, t, name, shape, dtype):
         """(pointer, position stride) of a channel-last (batch, seqlen, width) view: its last
         axis dense, its batch rows seqlen positions apart."""
+        if t is None:
+            return None, 0
         self.check(t, name, shape, dtype)
-        if t is None or not t.numel():
+        if not t.numel():
             return None, 0
         b, length, w = shape
         if w > 1 and t.stride(2) != 1:
@@ -64,8 +62,14 @@ class Call:
     def run(self, fn, args, stream):
         """Call the library with the tensors' device current, on `stream` or that device's
         current stream."""
-        if stream is not None and stream.device != self.device:
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-        with torch.cuda.device(self.device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            _abi.check(_abi.load(), fn(*args, ctypes.c_void_p(s.cuda_stream)))
+        if torch.cuda.current_device() == self.device.index:
+            status = fn(*args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, stream.cuda_stream)
+        if status:
+            _abi.check(_abi.load(), status)

@@ -330,7 +330,8 @@ template <int S, bool CL> struct BwdRun {
     __device__ __forceinline__ int t(int i) const { return CL ? tl : tl + i; }
 };
 
-// Per-channel constants in shared memory: 4 right-aligned taps, conv bias, dt bias, D.
+// Per-channel constants in shared memory: 4 right-aligned taps, conv bias, dt bias, D, and A
+// where it is per head.
 template <int S>
 __device__ __forceinline__ void load_prm(const BwdParams& p, int d0, float* prm) {
     using H = BwdShape<S>;
@@ -345,6 +346,7 @@ __device__ __forceinline__ void load_prm(const BwdParams& p, int d0, float* prm)
         prm[c * 8 + 4] = in && p.conv_w && p.conv_b ? p.conv_b[d] : 0.f;
         prm[c * 8 + 5] = in && p.dbias ? p.dbias[d] : 0.f;
         prm[c * 8 + 6] = in && p.D ? p.D[d] : 0.f;
+        prm[c * 8 + 7] = in && p.head_dim ? p.A[d / p.head_dim] : 0.f;
     }
 }
 
@@ -766,31 +768,47 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
     }
 }
 
-// A of one lane's 4 states (times log2 e), zeros past dim or d_state.
+// A of one lane's 4 states (times log2 e), zeros past dim or d_state. With A per head the
+// second pair holds what the product's rounding left: a head's dA sums over all its states and
+// channels, where an A off by 2^-25 shows (for single states it averages out).
 template <int S, bool HEADS>
-__device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_t (&A2)[2]) {
+__device__ __forceinline__ void load_A(const BwdParams& p, const float* prm, int c, int d, int j, uint64_t (&A2)[2]) {
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int n = 4 * j + (k ^ slot_order<S>(d));
-        const bool in = d < p.dim && n < p.dstate;
-        a[k] = !in ? 0.f : kLog2e * (HEADS ? p.A[d / p.head_dim] : p.A[(int64_t)d * p.dstate + n]);
+        const bool in = !HEADS && d < p.dim && n < p.dstate;
+        a[k] = in ? kLog2e * p.A[(int64_t)d * p.dstate + n] : 0.f;
     }
     A2[0] = pk2(a[0], a[1]);
     A2[1] = pk2(a[2], a[3]);
+    if constexpr (HEADS) {
+        constexpr float kLog2eRest = (float)(1.4426950408889634073599 - (double)kLog2e);
+        const float A = prm[c * 8 + 7];
+        const float hi = A * kLog2e, lo = fmaf(A, kLog2eRest, fmaf(A, kLog2e, -hi));
+        A2[0] = pk2(hi, hi);
+        A2[1] = pk2(lo, lo);
+    }
 }
 
 // Decay of one step for a lane's 4 states: 2^(delta A log2 e). With A per head one exp
 // serves all. d2: delta twice.
+// The SFU's exp comes out low on average: by 5e-9 to 8e-9 of its value for exponents above
+// -0.003, by 1.3e-8 to 2.9e-8 from there to -1 (means over 4 M random arguments each). A state
+// that decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which showed in
+// dA (2.5e-6 of its norm at the 130M layer's sizes, where an unbiased exp leaves 4e-7). The
+// exponent is therefore raised by the middle of that range, in the multiply that forms it.
+constexpr float kExpBias = 2.5e-8f;
 template <bool HEADS>
 __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint64_t (&a)[2]) {
     if constexpr (HEADS) {
-        const float e = ex2(lo2(d2) * lo2(A2[0]));
+        const float d = lo2(d2);
+        const float e = ex2(fmaf(d, lo2(A2[0]), fmaf(d, lo2(A2[1]), kExpBias)));
         a[0] = a[1] = pk2(e, e);
     } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const float2 x = upk2(mul2(d2, A2[k]));
+            const float2 x = upk2(fma2(d2, A2[k], pk2(kExpBias, kExpBias)));
             a[k] = pk2(ex2(x.x), ex2(x.y));
         }
     }
@@ -917,8 +935,8 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
     for (int kc = 0; kc < H::KC; ++kc)
 #pragma unroll
         for (int kl = 0; kl < KL; ++kl) {
-            const int d = d0 + H::channel(warp, kc, cl, j, kl);
-            load_A<S, HEADS>(p, d, j, A2[kc][kl]);
+            const int c = H::channel(warp, kc, cl, j, kl), d = d0 + c;
+            load_A<S, HEADS>(p, prm, c, d, j, A2[kc][kl]);
             R[kc][kl][0] = R[kc][kl][1] = 0;
             P[kc][kl][0] = P[kc][kl][1] = pk2(1.f, 1.f);
             h[kc][kl][0] = h[kc][kl][1] = 0;
@@ -1193,7 +1211,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
             if (te == L) load_state<S>(p, p.dhl, b, d, j, m[kl]);
             else if (d < p.dim) ldpair(p.sumR + ns_off<S>(p, row, d, j), m[kl]);
             if constexpr (REGS) {
-                load_A<S, HEADS>(p, d, j, A2[kl]);
+                load_A<S, HEADS>(p, prm, d - d0, d, j, A2[kl]);
             } else {
                 stpair(place(kc, kl), m[kl]);
                 stpair(place(kc, kl) + 4, dA[kl]);
@@ -1254,7 +1272,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                     const int c = H::channel(warp, kc, cl, j, kl);
                     so[kl] = c * (TT + 1) + sub * ST;
                     if constexpr (!REGS) {
-                        load_A<S, HEADS>(p, d0 + c, j, A2[kl]);
+                        load_A<S, HEADS>(p, prm, c, d0 + c, j, A2[kl]);
                         ldpair(place(kc, kl), m[kl]);
                         ldpair(place(kc, kl) + 4, dA[kl]);
                     }

@@ -3,12 +3,13 @@ between the forward and the backward pass (the training part of include/ssm.h)."
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _abi
-from ._marshal import Call, dtype_code
+from ._marshal import DTYPES, Call, dtype_code
 
 __all__ = ["ScanGrads", "ConvGrads", "Packed8", "ssm_selective_scan_bwd",
            "ssm_selective_scan_bwd_workspace_size", "ssm_causal_conv1d_bwd",
@@ -51,10 +52,26 @@ def _blocks(seqlen):
     return -(-seqlen // BLOCK)
 
 
-def _workspace_bytes(a):
+@functools.lru_cache(maxsize=256)
+def _scan_workspace(dtype, batch, dim, seqlen, dstate, a_heads, conv_width, packed, channel_last,
+                    num_segments):
+    """The library's answer for these sizes (it depends on nothing else)."""
     lib = _abi.load()
+    a = _abi.ScanBwdArgs()
+    a.dtype, a.batch, a.dim, a.seqlen, a.dstate, a.a_heads = dtype, batch, dim, seqlen, dstate, a_heads
+    a.conv_weight, a.conv_width = (1 if conv_width else None), conv_width
+    a.seq_starts, a.num_seqs = (1, 1) if packed else (None, 0)
+    a.channel_last, a.num_segments = channel_last, num_segments
     n = ctypes.c_size_t()
     _abi.check(lib, lib.ssm_selective_scan_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _conv_workspace(batch, dim, seqlen):
+    lib = _abi.load()
+    n = ctypes.c_size_t()
+    _abi.check(lib, lib.ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, ctypes.byref(n)))
     return n.value
 
 
@@ -62,13 +79,10 @@ def ssm_selective_scan_bwd_workspace_size(batch, dim, seqlen, dstate, dtype=torc
                                           conv_width=0, a_heads=0, packed_sequences=False,
                                           channel_last=False, num_segments=0):
     """Workspace bytes ssm_selective_scan_bwd needs for these sizes (host-only query)."""
-    a = _abi.ScanBwdArgs()
-    a.dtype = _abi.SSM_BF16 if dtype == torch.bfloat16 else _abi.SSM_F32
-    a.batch, a.dim, a.seqlen, a.dstate, a.a_heads = batch, dim, seqlen, dstate, a_heads
-    a.conv_weight, a.conv_width = (1 if conv_width else None), conv_width
-    a.seq_starts, a.num_seqs = (1, 1) if packed_sequences else (None, 0)
-    a.channel_last, a.num_segments = int(bool(channel_last)), num_segments
-    return _workspace_bytes(a)
+    if dtype not in DTYPES:
+        raise TypeError(f"activations must be float32 or bfloat16, got {dtype}")
+    return _scan_workspace(DTYPES[dtype], batch, dim, seqlen, dstate, a_heads, conv_width,
+                           int(bool(packed_sequences)), int(bool(channel_last)), num_segments)
 
 
 def ssm_selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None,
@@ -174,13 +188,13 @@ def ssm_selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=N
                  "dconv_history"):
         v = getattr(g, name)
         setattr(a, name, None if v is None else v.data_ptr() or None)
-    need = _workspace_bytes(a)
+    need = _scan_workspace(a.dtype, batch, dim, seqlen, n, a.a_heads, width, int(seq_starts is not None),
+                           a.channel_last, a.num_segments)
     if need:
         if workspace is None:
             workspace = new(need, torch.uint8)
-        call.check(workspace, "workspace", workspace.shape, torch.uint8)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
+        else:
+            call.ptr(workspace, "workspace", workspace.shape, torch.uint8)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     call.run(lib.ssm_selective_scan_bwd, (ctypes.byref(a),), stream)
     return g
@@ -202,11 +216,10 @@ def ssm_causal_conv1d_bwd(dout, x, w, bias=None, apply_silu=True, *, workspace=N
     pb = call.ptr(bias, "bias", (dim,), torch.float32)
     dx, dw = torch.empty_like(x), torch.empty_like(w)
     db = None if bias is None else torch.empty_like(bias)
-    n = ctypes.c_size_t()
-    _abi.check(lib, lib.ssm_causal_conv1d_bwd_workspace_size(batch, dim, seqlen, ctypes.byref(n)))
     if workspace is None:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=call.device)
-    call.ptr(workspace, "workspace", workspace.shape, torch.uint8)
+        workspace = torch.empty(_conv_workspace(batch, dim, seqlen), dtype=torch.uint8, device=call.device)
+    else:
+        call.ptr(workspace, "workspace", workspace.shape, torch.uint8)
     call.run(lib.ssm_causal_conv1d_bwd,
              (pd, px, pw, pb, dx.data_ptr() or None, dw.data_ptr() or None,
               None if db is None else db.data_ptr() or None, batch, dim, seqlen, width,

@@ -48,7 +48,7 @@ template <int S> struct BwdShape {
     static constexpr int W = S == 4 ? 2 : 4;                   // scan warps per CTA
     static constexpr int NH = S == 1 || S == 2 ? 128 : 64;     // helper threads
     static constexpr int NT = 32 * W + NH;
-    static constexpr int CTAS = S == 4 ? 3 : S == 8 ? 2 : 1;   // per SM, by registers and shared memory
+    static constexpr int CTAS = S == 4 ? 3 : S >= 8 ? 2 : 1;   // per SM, by registers and shared memory
     static constexpr int KC = S <= 8 ? 1 : S / 8;              // such groups a warp takes in turn
     static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
     static constexpr int G = W * CW * KL * KC;                 // channels per CTA
@@ -67,7 +67,8 @@ template <int S> struct BwdShape {
     static constexpr int kBC = NC * RQ;                        // begin 16 banks apart
     static constexpr int kStaged(bool adj) { return kSt + (adj ? kG + kU + 2 * kBC : kBC); }
     static constexpr int RP = 2 * NS + 8;                      // row of dB, dC of a step
-    static constexpr int kPart = W * TT * RP;
+    static constexpr int PS = S >= 16 ? T : TT;                // steps of dB, dC summed at a time
+    static constexpr int kPart = W * PS * RP;
     static constexpr int kPrm = 8 * G;
     static constexpr int kMask = 4;                            // sequence starts of the two tiles, as bits
     static constexpr int kSum = 2 * G * TT;                    // channel-last dD, dbias sums
@@ -1233,6 +1234,29 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
     for (int kl = 0; kl < KL; ++kl) hn[kl][0] = hn[kl][1] = 0;
     load_ckpt(0);
     int left = ntiles * H::NSUB;                               // sub-tiles to come
+    // the CTA's dB and dC of the PS steps from t on: the sum over its warps
+    auto flush = [&](int t) {
+        constexpr int ROW = 2 * H::NS, PS = H::PS;
+        named_bar_sync(2, 32 * H::W);
+        float* out = p.parts + (((int64_t)blockIdx.x * p.batch + b) * L + t) * ROW;
+        const int n = min(PS, te - t) * ROW;                   // below 1 past the segment's end
+#pragma unroll
+        for (int k = tid * 4; k < PS * ROW; k += 32 * H::W * 4) {
+            if (k >= n) break;
+            const float* from = part + k / ROW * H::RP + k % ROW;
+            float4 v = *reinterpret_cast<const float4*>(from);
+#pragma unroll
+            for (int w = 1; w < H::W; ++w) {
+                const float4 q = *reinterpret_cast<const float4*>(from + w * PS * H::RP);
+                v.x += q.x;
+                v.y += q.y;
+                v.z += q.z;
+                v.w += q.w;
+            }
+            *reinterpret_cast<float4*>(out + k) = v;
+        }
+        if (PS < TT) named_bar_sync(2, 32 * H::W);
+    };
     __syncthreads();                                           // tile 0 is staged
     for (int n = 0; n < ntiles; ++n) {
         const int tile = ntiles - 1 - n, t0 = tb + tile * TT;
@@ -1371,42 +1395,22 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                 const int first = Sums::first(lane);
 #pragma unroll
                 for (int k = 0; k < Sums::kept(); ++k) {
-                    float* o = part + (warp * TT + sub * ST + first + k) * H::RP + 4 * j + sq;
+                    float* o = part + (warp * H::PS + (H::PS == TT ? sub * ST : 0) + first + k) * H::RP + 4 * j + sq;
                     o[0] = rB[k];
                     o[H::NS] = rC[k];
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < ST * PT; ++k) {            // slot k % PT * NC of step k / PT
-                    float* o = part + (warp * TT + sub * ST + k / PT) * H::RP + 4 * j +
+                    float* o = part + (warp * H::PS + (H::PS == TT ? sub * ST : 0) + k / PT) * H::RP + 4 * j +
                                (k % PT * H::NC ^ sq);
                     o[0] = rB[k];
                     o[H::NS] = rC[k];
                 }
             }
+            if constexpr (H::PS == ST) flush(t0 + sub * ST);   // the next sub-tile takes its place
         }
-        // the CTA's dB and dC of the tile
-        if (H::W > 1) named_bar_sync(2, 32 * H::W);
-        {
-            constexpr int ROW = 2 * H::NS;
-            float* out = p.parts + (((int64_t)blockIdx.x * p.batch + b) * L + t0) * ROW;
-            const int n = min(TT, te - t0) * ROW;
-#pragma unroll
-            for (int k = tid * 4; k < TT * ROW; k += 32 * H::W * 4) {
-                if (k >= n) break;
-                const float* from = part + k / ROW * H::RP + k % ROW;
-                float4 v = *reinterpret_cast<const float4*>(from);
-#pragma unroll
-                for (int w = 1; w < H::W; ++w) {
-                    const float4 q = *reinterpret_cast<const float4*>(from + w * TT * H::RP);
-                    v.x += q.x;
-                    v.y += q.y;
-                    v.z += q.z;
-                    v.w += q.w;
-                }
-                *reinterpret_cast<float4*>(out + k) = v;
-            }
-        }
+        if constexpr (H::PS == TT) flush(t0);
         __syncthreads();                                       // tile n is done, n + 1 staged
     }
     // what the sweep summed over its steps

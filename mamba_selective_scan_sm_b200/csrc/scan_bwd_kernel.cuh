@@ -52,7 +52,7 @@ template <int S> struct BwdShape {
     static constexpr int KC = S <= 8 ? 1 : S / 8;              // such groups a warp takes in turn
     static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
     static constexpr int G = W * CW * KL * KC;                 // channels per CTA
-    static constexpr int TT = 8;                               // steps per tile
+    static constexpr int TT = S == 4 ? 16 : 8;                 // steps per tile
     static constexpr int NSUB = TT / T;
     static constexpr int EPT = G * TT / NH;                    // elements per helper and tensor
     static constexpr int RB = NS;                              // row of B / C in floats
@@ -67,7 +67,7 @@ template <int S> struct BwdShape {
     static constexpr int kBC = NC * RQ;                        // begin 16 banks apart
     static constexpr int kStaged(bool adj) { return kSt + (adj ? kG + kU + 2 * kBC : kBC); }
     static constexpr int RP = 2 * NS + 8;                      // row of dB, dC of a step
-    static constexpr int PS = S >= 16 ? T : TT;                // steps of dB, dC summed at a time
+    static constexpr int PS = S >= 16 || S == 4 ? T : TT;                // steps of dB, dC summed at a time
     static constexpr int kPart = W * PS * RP;
     static constexpr int kPrm = 8 * G;
     static constexpr int kMask = 4;                            // sequence starts of the two tiles, as bits
@@ -111,9 +111,9 @@ template <typename T, int S, bool CL> struct BwdRaw {
     static constexpr int DY = Z + kRows * kRow;
     static constexpr int B = DY + kRows * kRow;
     static constexpr int C = B + (CL ? H::TT : H::NS) * kBRow;
-    static constexpr int SC = C + (CL ? H::TT : H::NS) * kBRow;    // scales: 3 tensors x 2 blocks x G
-    static constexpr int SINCE = SC + 6 * H::G * 4;
-    static constexpr int BYTES = SINCE + 16;
+    static constexpr int SINCE = C + (CL ? H::TT : H::NS) * kBRow;
+    static constexpr int SC = SINCE + 16;                      // 8 bits: scales, 3 tensors x 2 blocks x G
+    static constexpr int bytes(bool q8) { return SC + (q8 ? 6 * H::G * 4 : 0); }
 };
 
 // f[i] = element lo..hi-1 of a run (others 0) at p + i * step; one 16-byte (or two, or one
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
     float* prm = sm + 2 * kStaged;
     uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
     uint8_t* raw = reinterpret_cast<uint8_t*>(prm + H::kPrm + H::kMask);
-    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
+    constexpr int kRaw = BwdRaw<T, S, CL>::bytes(Q8);
     using K = BwdCopies<T, S, CL, Q8, SUM>;
     BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 2 * kRaw);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -1067,7 +1067,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
     float* carry = prm + H::kPrm + H::kMask;
     float* sums = carry + H::kCarry;
     uint8_t* raw = reinterpret_cast<uint8_t*>(sums + (CL ? H::kSum : 0));
-    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES;
+    constexpr int kRaw = BwdRaw<T, S, CL>::bytes(Q8);
     using K = BwdCopies<T, S, CL, Q8, true>;
     BwdCopy* table = reinterpret_cast<BwdCopy*>(raw + 3 * kRaw);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;

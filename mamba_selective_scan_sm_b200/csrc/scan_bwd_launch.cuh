@@ -20,7 +20,7 @@ inline cudaError_t launch_with_smem(K k, dim3 grid, int threads, int smem, const
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
 inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t st) {
     using H = BwdShape<S>;
-    constexpr int kRaw = BwdRaw<T, S, CL>::BYTES, kHead = (H::kPrm + H::kMask) * 4;
+    constexpr int kRaw = BwdRaw<T, S, CL>::bytes(Q8), kHead = (H::kPrm + H::kMask) * 4;
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid, H::NT,

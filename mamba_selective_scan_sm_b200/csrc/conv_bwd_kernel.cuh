@@ -42,7 +42,7 @@ __device__ __forceinline__ void take_dense(const T* p, bool rev, float (&f)[R]) 
 }
 
 template <typename T, bool Q8>
-__global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const ConvBwdParams p) {
+__global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const ConvBwdParams p) {
     constexpr int R = kConvRun;
     using X = std::conditional_t<Q8, int8_t, T>;
     const int L = p.seqlen, dir = p.reverse ? -1 : 1;
@@ -77,35 +77,33 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
             scaled(run, R, pos0);
 #pragma unroll
             for (int i = 0; i < R; ++i) x[3 + i] = run[i];
-            if (t0 > 0) {
-                take_dense<X, 4>(xr + pos0 - dir * 4, rev, near);
-                scaled(near, 4, pos0 - dir * 4);
+            // (at a row's ends some other 4 of the row in their place, not used: no branch comes
+            // between the loads)
+            const bool more = t0 + R < L;
+            const int before = t0 > 0 ? pos0 - dir * 4 : pos0, after = more ? pos0 + dir * R : pos0;
+            take_dense<X, 4>(xr + before, rev, near);
+            scaled(near, 4, before);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) x[i] = near[i + 1];
+            for (int i = 0; i < 3; ++i) x[i] = near[i + 1];
+            take_dense<X, 4>(xr + after, rev, near);
+            scaled(near, 4, after);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) x[R + 3 + i] = more ? near[i] : 0.f;
+            if (p.dout32) {
+                const float* o = static_cast<const float*>(p.dout) + orow;
+                take_dense<float, R>(o + pos0, rev, run);
+                take_dense<float, 4>(o + after, rev, near);
             } else {
+                const T* o = static_cast<const T*>(p.dout) + orow;
+                take_dense<T, R>(o + pos0, rev, run);
+                take_dense<T, 4>(o + after, rev, near);
+            }
+            if (!more)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) near[i] = 0.f;
+            if (t0 == 0)
 #pragma unroll
                 for (int i = 0; i < 3; ++i) x[i] = conv_hist<T>(p, b, d, i - 3);
-            }
-            const bool more = t0 + R < L;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) near[i] = 0.f;
-            if (more) {
-                take_dense<X, 4>(xr + pos0 + dir * R, rev, near);
-                scaled(near, 4, pos0 + dir * R);
-            }
-#pragma unroll
-            for (int i = 0; i < 3; ++i) x[R + 3 + i] = near[i];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) near[i] = 0.f;
-            if (p.dout32) {
-                const float* o = static_cast<const float*>(p.dout) + orow + pos0;
-                take_dense<float, R>(o, rev, run);
-                if (more) take_dense<float, 4>(o + dir * R, rev, near);
-            } else {
-                const T* o = static_cast<const T*>(p.dout) + orow + pos0;
-                take_dense<T, R>(o, rev, run);
-                if (more) take_dense<T, 4>(o + dir * R, rev, near);
-            }
 #pragma unroll
             for (int i = 0; i < R + 3; ++i) dp[i] = i < R ? run[i < R ? i : 0] : near[i < R ? 0 : i - R];
         } else {
@@ -177,14 +175,9 @@ __global__ void __launch_bounds__(kConvRowThreads) conv_bwd_row_kernel(const Con
     }
 }
 
-// E values of x or dout at a step, as they come: VEC in one load where p.vec says that whole
-// runs are aligned to their size (a bf16 run of 4 in 8 bytes, fp32 in 16), else by element.
+// The first hi of E values at p, the others 0.
 template <typename Q, int E>
-__device__ __forceinline__ void take_or(const Q* p, bool vec, int hi, float (&f)[E]) {
-    if (vec && hi == E) {
-        take_run<Q, E>(p, false, f);
-        return;
-    }
+__device__ __forceinline__ void take_some(const Q* p, int hi, float (&f)[E]) {
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         f[i] = 0.f;
@@ -233,24 +226,40 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
     for (int lag = 0; lag < 3; ++lag) {
         const int t = tb - 1 - lag;
         if (t >= 0) {
-            take_or<X, E>(xb + (int64_t)pos(t) * p.x.s.p, p.vec, hi, xw[lag]);
+            take_some<X, E>(xb + (int64_t)pos(t) * p.x.s.p, hi, xw[lag]);
             scaled(t, xw[lag]);
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) xw[lag][i] = i < hi ? conv_hist<T>(p, b, d + i, t) : 0.f;
         }
     }
+    const bool whole = p.vec && hi == E;
     for (int tu = tb; tu < te + 3; tu += U) {
         float x[U][E], dp[U][E];
         int sn[U];
+        if (whole) {                                           // every load before the first use
 #pragma unroll
-        for (int k = 0; k < U; ++k) {                          // every load before the first use
-            const int t = tu + k, n = t < L && t < te + 3 ? hi : 0;
-            const int64_t ps = n ? pos(t) : 0;
-            take_or<X, E>(xb + ps * p.x.s.p, p.vec, n, x[k]);
-            take_or<float, E>(yb + ps * p.sdo.p, p.vec, n, dp[k]);
-            sn[k] = p.since && n ? p.since[t] : 4;
+            for (int k = 0; k < U; ++k) {
+                const int64_t ps = pos(min(tu + k, L - 1));    // past the end: the last step, dropped below
+                take_run<X, E>(xb + ps * p.x.s.p, false, x[k]);
+                take_run<float, E>(yb + ps * p.sdo.p, false, dp[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (tu + k >= L)
+#pragma unroll
+                    for (int i = 0; i < E; ++i) x[k][i] = dp[k][i] = 0.f;
+        } else {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int n = tu + k < L ? hi : 0;
+                const int64_t ps = n ? pos(tu + k) : 0;
+                take_some<X, E>(xb + ps * p.x.s.p, n, x[k]);
+                take_some<float, E>(yb + ps * p.sdo.p, n, dp[k]);
+            }
         }
+#pragma unroll
+        for (int k = 0; k < U; ++k) sn[k] = p.since ? p.since[min(tu + k, L - 1)] : 4;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int t = tu + k;

@@ -306,7 +306,8 @@ SSM_API ssm_status_t ssm_selective_scan_fwd_noalloc(const ssm_scan_args_t* args,
  * the two passes. Conventions as above: nothing is allocated, arguments are checked
  * before any launch, and the sums over batch, positions and channels are taken in fp32 in
  * a fixed order, so that a call repeated on the same inputs gives the same bits.
- */
+ * Calls that may run at the same time (other streams, graphs replayed side by side) need
+ * a workspace each. */
 
 /* Positions of a channel that share one scale of an 8-bit activation. */
 #define SSM_CHECKPOINT_BLOCK 64

@@ -170,7 +170,8 @@ ssm_status_t ssm_checkpoint_pack(const void* x, void* codes, float* scales, int6
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
     if (ranges_overlap(outs[0].p, outs[0].bytes, outs[1].p, outs[1].bytes))
         return api_fail(SSM_ERR_ALIAS, "codes overlaps scales");
-    PackParams p{x, sx, static_cast<int8_t*>(codes), scales, nullptr, (int)batch, (int)dim, (int)seqlen};
+    PackParams p{x, sx, static_cast<int8_t*>(codes), scales, nullptr, (int)batch, (int)dim, (int)seqlen,
+                 is_aligned(x, 16) && sx % 8 == 0};
     cudaError_t e = launch_pack((int)es, channel_last != 0, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? api_ok() : api_cuda(e, "pack launch");
 }
@@ -191,7 +192,7 @@ ssm_status_t ssm_checkpoint_unpack(const void* codes, const float* scales, void*
     if ((status = check_aligned(outs)) != SSM_OK) return status;
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
     PackParams p{nullptr, 0, static_cast<int8_t*>(const_cast<void*>(codes)), const_cast<float*>(scales),
-                 out, (int)batch, (int)dim, (int)seqlen};
+                 out, (int)batch, (int)dim, (int)seqlen, 0};
     cudaError_t e = launch_unpack((int)es, channel_last != 0, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? api_ok() : api_cuda(e, "unpack launch");
 }
@@ -223,6 +224,8 @@ ssm_status_t ssm_state_cache_write(const float* state, void* codes, float* scale
     p.slots = slots;
     p.rand = rand;
     p.state = state;
+    // every lane of a row holds 8 states of it, at a multiple of 32 bytes
+    p.vec = (dstate & (dstate - 1)) == 0 && dstate >= 8 && is_aligned(state, 16);
     cudaError_t e = launch_cache_write(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? api_ok() : api_cuda(e, "cache write launch");
 }

@@ -231,14 +231,22 @@ __global__ void __launch_bounds__(256) pack_cl_kernel(const PackParams p) {
         const int t0 = blk * kBlock8 + warp * 8;
         float x[8][8];                                         // [channel][position]
         float top[8];
+        const T* src = static_cast<const T*>(p.x) + (int64_t)b * p.seqlen * p.sx + d;
+        if (p.vec && hi == 8) {                                // every load before the first use
+            float v[8][8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int t = t0 + r;
-            float v[8];
-            load_run<T, 8>(static_cast<const T*>(p.x) + ((int64_t)b * p.seqlen + t) * p.sx + d, 1, 0,
-                           t < p.seqlen ? hi : 0, v);
+            for (int r = 0; r < 8; ++r)
+                take_run<T, 8>(src + (int64_t)min(t0 + r, p.seqlen - 1) * p.sx, false, v[r]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i][r] = v[i];
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i][r] = t0 + r < p.seqlen ? v[r][i] : 0.f;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i][r] = t0 + r < p.seqlen && i < hi ? Elem<T>::to_f(src[(int64_t)(t0 + r) * p.sx + i]) : 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -332,7 +340,9 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheParams p) {
             const int64_t slot = slot_of(p, b);
             if (slot >= 0) at[k] = slot * dim + (row - b * dim);
         }
-        load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, 1, 0, at[k] >= 0 ? n : 0, h[k]);
+        // whole, aligned rows: no branch comes between the loads
+        if (p.vec) take_run<float, 8>(p.state + (int64_t)min(row, rows - 1) * p.dstate + 8 * j, false, h[k]);
+        else load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, 1, 0, at[k] >= 0 ? n : 0, h[k]);
     }
 #pragma unroll
     for (int k = 0; k < kCacheRows; ++k) {

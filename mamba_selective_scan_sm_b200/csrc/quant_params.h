@@ -13,6 +13,7 @@ struct PackParams {
     float* scales;
     void* out;                    // unpack
     int batch, dim, seqlen;
+    int vec;                      // channel-last x: runs of 8 channels are aligned to their size
 };
 
 struct CacheParams {
@@ -23,6 +24,7 @@ struct CacheParams {
     const int32_t* slots;
     const uint32_t* rand;
     const float* state;           // write
+    int vec;                      // write: rows of whole aligned lanes (dstate 8, 16, 32, 64 or 128)
     void* out;                    // read, update
     // update
     void* conv_state;

@@ -153,6 +153,27 @@ def test_cache_special_rows():
     assert np.all(np.isnan(back[:2])) and np.all(back[2:4] == 0) and np.all(np.isfinite(back[4]))
 
 
+def test_a_cache_past_32_bit_offsets():
+    """Slots whose codes lie past 2^31 bytes, at both ends of the cache."""
+    m = ssm()
+    num, dim, n = 70000, 2048, 16
+    codes = torch.zeros(num, dim, n, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(num, dim, device="cuda")
+    state = torch.randn(3, dim, n, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    slots = torch.tensor([num - 1, 0, 67000], dtype=torch.int32, device="cuda")
+    m.ssm_state_cache_write(state, codes, scales, slots=slots)
+    back = m.ssm_state_cache_read(codes, scales, slots=slots)
+    top = state.abs().amax(-1, keepdim=True)
+    assert torch.all((back - state).abs() <= top / 254 * (1 + 1e-5))
+    one = torch.zeros(3, dim, device="cuda")
+    bc = torch.ones(3, n, device="cuda")
+    y = m.ssm_selective_state_update_cached(codes, scales, None, one, one, torch.zeros(dim, n, device="cuda"), bc, bc,
+                                            dt_softplus=False, slots=slots)
+    assert torch.allclose(y, back.sum(-1), rtol=1e-5, atol=1e-5)
+    assert torch.equal(m.ssm_state_cache_read(codes, scales, slots=slots), back)
+    assert not codes[1:67000].any() and not codes[67001:num - 1].any()
+
+
 def test_dither_is_right_on_average():
     """A value a fifth of a step above a code: over random bits the stored mean is the value.
     4096 draws of a step's fraction have a standard error of 0.4 / 64 = 0.00625 steps; the

@@ -118,6 +118,60 @@ def test_segments_states(N):
     run(case(8, "f32", 1, 33, 90, N, h0=True, dfinal=True), "f32", num_segments=3)
 
 
+@pytest.mark.parametrize("cl", [False, True])
+@pytest.mark.parametrize("L", [1, 2, 3, 5])
+@pytest.mark.parametrize("width", [2, 3, 4])
+def test_short_continued(cl, L, width):
+    """Continued pieces shorter than the conv's window: the history's gradient reaches past them."""
+    run(case(24, "f32", 2, 35, L, 16, conv=width, h0=True, hist=True, dfinal=True), "f32", cl)
+
+
+@pytest.mark.parametrize("N", [16, 128])
+def test_two_pieces_are_one_sequence(N):
+    """The gradients of a sequence taken in two pieces: the second piece's dinitial_state and
+    dconv_history go into the first one's dfinal_state and its last inputs."""
+    L, cut, W = 60, 23, 4
+    c = case(25, "f32", 1, 36, L, N, conv=W, h0=True, hist=True, dfinal=True)
+    whole = reference(c)
+    cuts = {k: (v[:, :, :cut], v[:, :, cut:]) for k, v in c.items() if k in ("u", "delta", "B", "C", "z", "dout")}
+    first = dict(c, **{k: v[0] for k, v in cuts.items()}, dfinal=None)
+    m, f = ssm(), (lambda v: gpu(v, "f32"))
+    _, h = m.ssm_selective_scan_fwd(f(first["u"]), f(first["delta"]), f(c["A"]), f(first["B"]), f(first["C"]),
+                                    f(c["D"]), f(first["z"]), f(c["delta_bias"]), True, False, f(c["conv_w"]),
+                                    f(c["conv_b"]), return_final_state=True, initial_state=f(c["h0"]),
+                                    conv_history=f(c["hist"]))
+    second = dict(c, **{k: v[1] for k, v in cuts.items()}, h0=host(h), hist=c["u"][:, :, cut - W + 1:cut])
+    second["h0"] = second["h0"].astype(np.float32)
+    b = call(second, "f32")
+    a = call(dict(first, dfinal=host(b.dinitial_state).astype(np.float32)), "f32")
+    du = np.concatenate([host(a.du), host(b.du)], 2)
+    du[:, :, cut - W + 1:cut] += host(b.dconv_history)
+    check("du", du, whole["du"], "f32")
+    for k in ("dA", "dD", "ddelta_bias", "dconv_weight", "dconv_bias"):
+        check(k, host(getattr(a, k)) + host(getattr(b, k)), whole[k], "f32")
+    check("dinitial_state", host(a.dinitial_state), whole["dinitial_state"], "f32")
+
+
+def test_guards_around_the_outputs():
+    """Nothing is written beside the outputs and the workspace."""
+    m = ssm()
+    c = case(26, "bf16", 1, 37, 45, 16, conv=4)
+    B, D, L, N = 1, 37, 45, 16
+
+    def guarded(n, dtype):
+        buf = torch.full((n + 256,), 7, dtype=dtype, device="cuda")
+        return buf, buf[128:128 + n]
+    outs = {k: guarded(n, torch.bfloat16) for k, n in (("du", D * L), ("ddelta", D * L), ("dz", D * L),
+                                                       ("dB", N * L), ("dC", N * L))}
+    need = m.ssm_selective_scan_bwd_workspace_size(B, D, L, N, conv_width=4)
+    ws, inner = guarded(need, torch.uint8)
+    view = {k: v[1].view(1, -1, L) for k, v in outs.items()}
+    g = call(c, "bf16", workspace=inner, **view)
+    compare(g, reference(c), "bf16")
+    for buf in [v[0] for v in outs.values()] + [ws]:
+        assert torch.all(buf[:128] == 7) and torch.all(buf[-128:] == 7)
+
+
 def test_extreme_values():
     """Large and very negative pre-softplus deltas, gates and conv outputs: decays that
     underflow to 0 and deltas near 0 leave finite gradients."""

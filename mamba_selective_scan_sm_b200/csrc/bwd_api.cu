@@ -87,20 +87,21 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     // Segments. One sweep per row takes two exps per (channel, step, state), segments a third
     // and one more pass over the inputs (about 1.3 times the time where one sweep per row fills
     // the GPU): so a grid that fills three quarters of the SMs' CTA slots is left alone. A
-    // smaller one is split so that its waves of CTAs, each as long as a segment, take the least
-    // time together, up to some four waves (measured: B8 D1536 L2048 1.10 ms in one sweep, 1.32
-    // in 9 segments; B4 D1536 L2048 1.15 in one, 0.90 in 9; B1 D5120 L16384 6.45 in one, 3.6
-    // in 9 to 27; d_state 128 with A per head, B2 D1536 L2048, 2.51 in one, 1.99 in 3).
+    // smaller one is split so that the waves of CTAs, each as long as a segment's tiles, and the
+    // chain over the segments take the least time together: some 7.5 us a tile and 0.3 us a
+    // segment (measured: B8 D1536 L2048 1.00 ms in one sweep, 1.2 in 6 segments; B4 D1536 L2048
+    // 0.88 in one, 0.71 in 6; B1 D5120 L16384 6.0 in one, 3.35 in 9; d_state 128 with A per
+    // head, B2 D1536 L2048, 2.48 in one, 1.66 in 3).
     int64_t nseg = a->num_segments;
     if (nseg == 0) {
         const int64_t ctas = pl->groups * Bn, slots = (int64_t)kNumSMs * pl->v.ctas;
         nseg = 1;
         if (ctas > 0 && 4 * ctas < 3 * slots) {
             double best = 1e30;
-            const int64_t most = std::min<int64_t>(ntiles, 4 * slots / ctas);
+            const int64_t most = std::min<int64_t>({ntiles, 4 * slots / ctas, 1024});
             for (int64_t n = 1; n <= most; ++n) {
-                const double waves = (double)((ctas * n + slots - 1) / slots);
-                const double t = waves / n + 0.002 * n + (n > 1 ? 0.1 * waves / n : 0.0);
+                const int64_t waves = (ctas * n + slots - 1) / slots, tiles = (ntiles + n - 1) / n;
+                const double t = waves * tiles * 7.5 * (n > 1 ? 1.1 : 1.0) + 0.3 * n;
                 if (t < best) {
                     best = t;
                     nseg = n;

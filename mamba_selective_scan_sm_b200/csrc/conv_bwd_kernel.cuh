@@ -3,10 +3,12 @@
 //   dpre_t = dout_t silu'(pre_t)                       (dout_t without the SiLU)
 //   dx_s   = sum_lag w[lag] dpre_{s+lag},   dw[lag] = sum_t dpre_t x_{t-lag},   db = sum_t dpre_t
 // lag = 0 .. W-1 (w here by lag, w[W-1-k] of the taps). Reads x and dout once, writes dx
-// once: bound by memory. Along a row a thread takes 8 steps and recomputes the 3 steps
-// behind them, whose dpre reach back into its own; channel-last a thread walks a run of
-// channels down a chunk of steps with the last 3 steps in registers. dw and db are summed
-// per CTA into a partial row each, and over the rows by conv_reduce_kernel: no atomics.
+// once. Along a row a thread takes 16 steps and recomputes the 3 steps behind them, whose dpre
+// reach back into its own (8 steps: 72 us against 60 at B8 D1536 L2048 bf16, where HBM needs
+// 23: the issue slots bind, 48 instructions an element); channel-last a thread walks a run of 4
+// channels down a chunk of 64 steps with the last 3 steps in registers, 4 steps' loads issued
+// together (32768 x 1536: 187 us, HBM 61). dw and db are summed per CTA into a partial row
+// each, and over the rows by conv_reduce_kernel: no atomics.
 #pragma once
 
 #include "scan_bwd_kernel.cuh"

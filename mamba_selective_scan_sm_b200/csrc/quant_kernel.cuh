@@ -1,7 +1,8 @@
 // 8-bit kernels for sm_100a: activations packed for a backward pass, and the decode states'
 // cache. A group (64 positions of a channel, or a channel's row of states) is held as int8
-// codes round(127 x / max|x|) and one fp32 scale max|x| / 127. All are bound by memory:
-// each value is read once and each code written once.
+// codes round(127 x / max|x|) and one fp32 scale max|x| / 127. Each value is read once and
+// each code written once; what binds is the issue slots (B8 D1536 L2048 bf16: pack 24 us, 83 %
+// busy, unpack 17 us, 79 %; HBM alone would take 11.5 each).
 //
 // Rounding. x (127 / max) + 1.5 2^23 in one fused operation leaves the rounded quotient in
 // the sum's low bits. The reciprocal is the SFU's (relative error below 2^-22), so the
@@ -61,28 +62,35 @@ struct Quant {
         }
     }
     // The same for values that are hardly ever next to a border (fp32 states): one test for
-    // all N, pairs at a time.
-    template <int N> __device__ __forceinline__ void nearest_rare(const float (&x)[N], uint32_t (&q)[N]) const {
+    // all N, pairs at a time. Without EXACT the fp32 quotient decides borders too: for values
+    // that carry roundings of their own (a state just computed).
+    template <bool EXACT, int N> __device__ __forceinline__ void nearest_rare(const float (&x)[N], uint32_t (&q)[N]) const {
         const uint64_t inv2 = pk2(inv, inv), magic2 = pk2(kMagic, kMagic), minus = pk2(-1.f, -1.f);
         float worst = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             const uint64_t x2 = pk2(x[i], x[i + 1]), t = fma2(x2, inv2, magic2);
-            const float2 err = upk2(fma2(x2, inv2, fma2(t, minus, magic2)));
-            worst = max_mag(worst, err.x, err.y);
+            if constexpr (EXACT) {
+                const float2 err = upk2(fma2(x2, inv2, fma2(t, minus, magic2)));
+                worst = max_mag(worst, err.x, err.y);
+            }
             const float2 f = upk2(t);
             q[i] = __float_as_uint(f.x);
             q[i + 1] = __float_as_uint(f.y);
         }
-        if (worst > kNear) nearest(x, q);                      // (NaN: a row that is not finite)
+        if (EXACT && worst > kNear) nearest(x, q);             // (NaN: a row that is not finite)
     }
     // floor(127 x / top + offset), the offset of value i the top 24 bits of bits + i GOLDEN as
     // a fraction. F = 1 + offset (to 23 bits: the 24th counts next to a border only) comes out
     // of one funnel shift, and x inv + F plus 1.5 2^23 - 1, rounded down, holds the code.
     // Offsets are random, so quotients next to a border are rare: fp64 there.
-    template <int N>
+    template <bool EXACT, int N>
     __device__ __forceinline__ void dithered(const float (&x)[N], uint32_t bits, uint32_t (&q)[N]) const {
-        const uint64_t inv2 = pk2(inv, inv), magic2 = pk2(kMagic - 1.f, kMagic - 1.f), minus = pk2(-1.f, -1.f);
+        // Without the exact test nothing else keeps max / max * 127 + offset below 128: the
+        // quotients are taken 2^-21 smaller, which is more than the reciprocal's and the
+        // product's rounding together.
+        const float by = EXACT ? inv : inv * 0.9999995231628418f;
+        const uint64_t inv2 = pk2(by, by), magic2 = pk2(kMagic - 1.f, kMagic - 1.f), minus = pk2(-1.f, -1.f);
         const uint64_t half2 = pk2(-0.5f, -0.5f);
         float worst = 0.f;
 #pragma unroll
@@ -93,14 +101,15 @@ struct Quant {
             const uint64_t v = fma2(pk2(x[i], x[i + 1]), inv2, f2);
             uint64_t t;
             asm("add.rm.f32x2 %0, %1, %2;" : "=l"(t) : "l"(v), "l"(magic2));
-            // v less its floor, less a half
-            const float2 e = upk2(add2(add2(v, half2), fma2(t, minus, magic2)));
-            worst = max_mag(worst, e.x, e.y);
+            if constexpr (EXACT) {                             // v less its floor, less a half
+                const float2 e = upk2(add2(add2(v, half2), fma2(t, minus, magic2)));
+                worst = max_mag(worst, e.x, e.y);
+            }
             const float2 f = upk2(t);
             q[i] = __float_as_uint(f.x);
             q[i + 1] = __float_as_uint(f.y);
         }
-        if (worst > kNear && inv != 0.f) {
+        if (EXACT && worst > kNear && inv != 0.f) {
 #pragma unroll 1
             for (int i = 0; i < N; ++i) {
                 float v = x[0];
@@ -132,13 +141,14 @@ struct Quant {
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// Four codes as floats: a byte plus 128 in the low bits of 2^23, less 2^23 + 128.
-__device__ __forceinline__ void unpack4(uint32_t w, float* f) {
+// Four codes as two pairs of floats: a byte plus 128 in the low bits of 2^23, less 2^23 + 128.
+__device__ __forceinline__ void unpack4(uint32_t w, uint64_t (&v)[2]) {
     w ^= 0x80808080u;
-    f[0] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - 8388736.f;
-    f[1] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - 8388736.f;
-    f[2] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - 8388736.f;
-    f[3] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - 8388736.f;
+    const uint64_t less = pk2(-8388736.f, -8388736.f);
+    v[0] = add2(pk2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)),
+                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441))), less);
+    v[1] = add2(pk2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)),
+                    __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443))), less);
 }
 
 // N codes of a run (a multiple of 4): whole and aligned in one access, else byte by byte.
@@ -191,7 +201,14 @@ __device__ __forceinline__ void load_codes(const int8_t* p, int hi, float (&f)[N
     uint32_t w[N / 4];
     load_code_words<N>(p, hi, w);
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) unpack4(w[i], f + 4 * i);
+    for (int i = 0; i < N / 4; ++i) {
+        uint64_t v[2];
+        unpack4(w[i], v);
+        f[4 * i] = lo2(v[0]);
+        f[4 * i + 1] = hi2(v[0]);
+        f[4 * i + 2] = lo2(v[1]);
+        f[4 * i + 3] = hi2(v[1]);
+    }
 }
 
 // ------------------------------------------------------------------ activations --
@@ -308,15 +325,15 @@ __device__ __forceinline__ int64_t slot_of(const CacheParams& p, int64_t b) {
 
 // Codes of a row's NP states from first on, and what the row's scale comes from, from LPR
 // lanes of a row.
-template <int LPR, int NP>
+template <bool EXACT, int LPR, int NP>
 __device__ __forceinline__ Quant quantise_row(const float (&h)[NP], const uint32_t* rand, int first,
                                               uint32_t (&q)[NP]) {
     float top = max_mag(h);
 #pragma unroll
     for (int w = 1; w < LPR; w *= 2) top = max_mag(top, top, __shfl_xor_sync(0xffffffffu, top, w));
     const Quant qz(top);
-    if (rand) qz.dithered(h, *rand + (uint32_t)first * 0x9E3779B9u, q);
-    else qz.nearest_rare(h, q);
+    if (rand) qz.dithered<EXACT>(h, *rand + (uint32_t)first * 0x9E3779B9u, q);
+    else qz.nearest_rare<EXACT>(h, q);
     return qz;
 }
 
@@ -348,7 +365,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheParams p) {
     for (int k = 0; k < kCacheRows; ++k) {
         uint32_t q[8];
         const uint32_t* rand = p.rand ? p.rand + (at[k] >= 0 ? r0 + k * per : 0) : nullptr;
-        const Quant qz = quantise_row<LPR, 8>(h[k], rand, 8 * j, q);
+        const Quant qz = quantise_row<true, LPR, 8>(h[k], rand, 8 * j, q);
         if (at[k] < 0) continue;
         if (n > 0) store_codes<8>(p.codes + at[k] * p.dstate + 8 * j, n, q);
         if (j == 0) p.scales[at[k]] = qz.scale();
@@ -379,7 +396,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheParams p) {
 // out. ASYNC: codes, scale, conv window and rounding bits come through a ring of asynchronous
 // copies kUpdateStages - 1 rows ahead (rows of 16-byte aligned codes, conv width 4 or none);
 // a thread reads back only what it copied itself. The rows' B and C are staged once as fp32
-// for all channels of the CTA.
+// for all channels of the CTA. B256 D5120 N16 bf16 with conv and rounding bits: 43 us, 94 MB
+// (14 us of HBM): some 520 instructions a row and channel at 0.6 of the issue rate (one row a
+// thread with plain loads: 124 us).
 constexpr int kUpdateThreads = 128;
 constexpr int kUpdateCtas = 4;                                 // per SM: 128 registers a thread
 // Most batch rows of a CTA (their B and C take 8 KB at most).
@@ -546,7 +565,7 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
             if constexpr (HEADS) one = ex2(dl * A2[0]);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                float c[4];
+                uint64_t c[2];
                 unpack4(v.codes[g], c);
                 const ulonglong2 b2 = Bv[g], c2 = Cv[g];
 #pragma unroll
@@ -557,7 +576,7 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
                         const float2 e = upk2(mul2(d2, pk2(A2[i], A2[i + 1])));
                         a = pk2(ex2(e.x), ex2(e.y));
                     }
-                    const uint64_t hn = fma2(a, mul2(pk2(c[2 * k], c[2 * k + 1]), s2), mul2(du2, k ? b2.y : b2.x));
+                    const uint64_t hn = fma2(a, mul2(c[k], s2), mul2(du2, k ? b2.y : b2.x));
                     y2 = fma2(hn, k ? c2.y : c2.x, y2);
                     const float2 f = upk2(hn);
                     h[i] = f.x;
@@ -570,7 +589,7 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
 #pragma unroll
         for (int k = 1; k < LPR; k *= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
         uint32_t q[16];
-        const Quant qz = quantise_row<LPR, 16>(h, p.rand ? &v.rand : nullptr, 16 * j, q);
+        const Quant qz = quantise_row<false, LPR, 16>(h, p.rand ? &v.rand : nullptr, 16 * j, q);
         if (!live) continue;
         if (n > 0) store_codes<16>(codes_at(at), n, q);
         if (j == 0) {

@@ -236,6 +236,32 @@ def test_decode_on_the_cache(dtype, dim, n, heads, conv, z):
     assert torch.equal(codes[1], kept[0]) and torch.equal(scales[2], kept[1])
 
 
+@pytest.mark.parametrize("n", [3, 16, 48])
+def test_the_largest_state_keeps_its_code(n):
+    """Rounding offsets next to 1 on the row's largest state, of either sign: 127 plus the offset
+    stays below 128 whatever the fp32 reciprocal does, over many magnitudes. (The step takes the
+    quotient within 1e-4: -127 plus such an offset may come out as -127 or -126.)"""
+    m = ssm()
+    rows = 20000
+    g = torch.Generator(device="cuda").manual_seed(2)
+    top = torch.exp(torch.rand(rows, 1, generator=g, device="cuda") * 40 - 20)
+    for at in (0, n - 1):
+        offset = (0xFFFFFFFF - at * 0x9E3779B9) & 0xFFFFFFFF          # state `at` gets the last offset
+        rand = torch.full((rows, 1), offset - (1 << 32) if offset >> 31 else offset, dtype=torch.int32, device="cuda")
+        for sign in (1.0, -1.0):
+            state = 0.3 * top[..., None] * (2 * torch.rand(rows, 1, n, generator=g, device="cuda") - 1)
+            state[:, 0, at] = sign * top[:, 0]
+            codes = torch.zeros(rows, 1, n, dtype=torch.int8, device="cuda")
+            scales = torch.zeros(rows, 1, device="cuda")
+            m.ssm_state_cache_write(state, codes, scales, rand=rand)
+            want = 127 if sign > 0 else -127
+            for _ in range(2):
+                assert bool((codes[:, 0, at] == want).all() if sign > 0 else (codes[:, 0, at] <= -126).all())
+                zero, bc = torch.zeros(rows, 1, device="cuda"), torch.zeros(rows, n, device="cuda")
+                m.ssm_selective_state_update_cached(codes, scales, None, zero, zero, torch.zeros(1, n, device="cuda"),
+                                                    bc, bc, dt_softplus=False, rand=rand)
+
+
 def test_a_state_decays_only_when_dithered():
     """delta A small enough that one token decays a state by less than half a step: rounding
     to the nearest keeps it where it is, dithered rounding loses it at the right rate."""

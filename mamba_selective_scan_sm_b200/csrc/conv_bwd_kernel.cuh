@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const 
     using X = std::conditional_t<Q8, int8_t, T>;
     const int L = p.seqlen, dir = p.reverse ? -1 : 1;
     const int64_t rowid = (int64_t)blockIdx.z * 65535 + blockIdx.y;
-    if (rowid >= (int64_t)p.batch * p.dim) return;
-    const int b = (int)(rowid / p.dim), d = (int)(rowid % p.dim);
+    if (rowid >= (int64_t)p.batch * p.dim) return;             // below 2^31: a 32-bit division
+    const int b = (int)((uint32_t)rowid / (uint32_t)p.dim), d = (int)((uint32_t)rowid % (uint32_t)p.dim);
     const int t0 = blockIdx.x * kConvRowChunk + threadIdx.x * R;
     float w[4];                                                // by lag
 #pragma unroll

@@ -213,6 +213,18 @@ __device__ __forceinline__ void load_codes(const int8_t* p, int hi, float (&f)[N
 
 // ------------------------------------------------------------------ activations --
 
+// i / n and i % n; in 32 bits where i allows it (a 64-bit division takes some 80 instructions).
+__device__ __forceinline__ void divide(int64_t i, uint32_t n, int64_t& q, int& r) {
+    if (i >> 32 == 0) {
+        const uint32_t k = (uint32_t)i / n;
+        q = k;
+        r = (int)((uint32_t)i - k * n);
+    } else {
+        q = i / n;
+        r = (int)(i - q * n);
+    }
+}
+
 // (batch, dim, seqlen): 8 neighbouring lanes hold a block of 64 positions.
 template <typename T>
 __global__ void __launch_bounds__(256) pack_row_kernel(const PackParams p) {
@@ -220,8 +232,10 @@ __global__ void __launch_bounds__(256) pack_row_kernel(const PackParams p) {
     const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x, blk = idx / 8;
     const int64_t rows = (int64_t)p.batch * p.dim;
     const bool in = blk < rows * nb;
-    const int64_t row = in ? blk / nb : 0;
-    const int t = in ? (int)(blk % nb) * kBlock8 + (int)(idx % 8) * 8 : p.seqlen;
+    int64_t row;
+    int first;
+    divide(in ? blk : 0, nb, row, first);
+    const int t = in ? first * kBlock8 + (int)(idx % 8) * 8 : p.seqlen;
     const int hi = min(8, p.seqlen - t);
     float x[8];
     load_run<T, 8>(static_cast<const T*>(p.x) + row * p.seqlen + t, 1, 0, hi, x);
@@ -295,15 +309,19 @@ __global__ void __launch_bounds__(256) pack_cl_kernel(const PackParams p) {
 template <typename T, bool CL>
 __global__ void __launch_bounds__(256) unpack_kernel(const PackParams p) {
     const int inner = CL ? p.dim : p.seqlen, runs = (inner + 7) / 8;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x, row = idx / runs;
+    int64_t row;
+    int run;
+    divide((int64_t)blockIdx.x * 256 + threadIdx.x, runs, row, run);
     const int nb = (p.seqlen + kBlock8 - 1) / kBlock8;
     if (row >= (int64_t)p.batch * (CL ? p.seqlen : p.dim)) return;
-    const int k = (int)(idx % runs) * 8, hi = min(8, inner - k);
+    const int k = run * 8, hi = min(8, inner - k);
     float f[8];
     load_codes<8>(p.codes + row * inner + k, hi, f);
     if constexpr (CL) {
-        const int64_t b = row / p.seqlen;
-        const int blk = (int)(row % p.seqlen) / kBlock8;
+        int64_t b;
+        int t;
+        divide(row, p.seqlen, b, t);
+        const int blk = t / kBlock8;
         float s[8];
         load_run<float, 8>(p.scales + (b * nb + blk) * p.dim + k, 1, 0, hi, s);
 #pragma unroll

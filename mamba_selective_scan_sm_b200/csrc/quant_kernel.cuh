@@ -414,9 +414,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheParams p) {
 // out. ASYNC: codes, scale, conv window and rounding bits come through a ring of asynchronous
 // copies kUpdateStages - 1 rows ahead (rows of 16-byte aligned codes, conv width 4 or none);
 // a thread reads back only what it copied itself. The rows' B and C are staged once as fp32
-// for all channels of the CTA. B256 D5120 N16 bf16 with conv and rounding bits: 43 us, 94 MB
-// (14 us of HBM): some 520 instructions a row and channel at 0.6 of the issue rate (one row a
-// thread with plain loads: 124 us).
+// for all channels of the CTA. B256 D5120 N16 bf16 with conv and rounding bits: 28 us, 94 MB
+// (14 us of HBM); the issue slots bind (one row a thread with plain loads: 124 us; with
+// quotients next to a border decided exactly: 43 us).
 constexpr int kUpdateThreads = 128;
 constexpr int kUpdateCtas = 4;                                 // per SM: 128 registers a thread
 // Most batch rows of a CTA (their B and C take 8 KB at most).

@@ -75,7 +75,10 @@ template <int S> struct BwdShape {
     static constexpr int kOut = G * RO;                        // one of y, s1, s2
     static constexpr int RQ = TT * RB + 16;                    // one order's copy of B / C: the copies
     static constexpr int kBC = NC * RQ;                        // begin 16 banks apart
-    static constexpr int kStaged(bool adj) { return kSt + (adj ? kG + kU + 2 * kBC : kBC); }
+    static constexpr int kDecay = G * (TT + 1);                // A per head: decays
+    static constexpr int kStaged(bool adj, bool heads) {
+        return kSt + (heads ? kDecay : 0) + (adj ? kG + kU + 2 * kBC : kBC);
+    }
     static constexpr int RP = 2 * NS + 8;                      // row of dB, dC of a step
     static constexpr int PS = S >= 16 || S == 4 ? T : TT;                // steps of dB, dC summed at a time
     static constexpr int kPart = W * PS * RP;
@@ -638,10 +641,10 @@ __device__ __forceinline__ void each_pair(float (&out)[E], const float (&in)[E],
 // step, g and u where ADJ, and the rows of B (and C
 // where ADJ) in each order of the states. Steps past the end and channels past dim get
 // zeros: a = 1 and no input, which leave both recurrences where they are.
-template <typename T, int S, bool CL, bool Q8, bool ADJ>
+template <typename T, int S, bool CL, bool Q8, bool ADJ, bool HEADS>
 __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, int d0, int t0, const uint8_t* raw,
-                                           const float* prm, float2* st, float* gs, float* us,
-                                           float* Bs, float* Cs, uint32_t* mask) {
+                                           const float* prm, float2* st, float* as, float* gs,
+                                           float* us, float* Bs, float* Cs, uint32_t* mask) {
     using H = BwdShape<S>;
     using R = BwdRaw<T, S, CL>;
     constexpr int E = H::EPT;
@@ -748,6 +751,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
         const int o = r.c(i) * (H::TT + 1) + r.t(i);
         const float du = dl * u[i];
         st[o] = make_float2(dl, du);
+        if constexpr (HEADS) as[o] = expf(dl * prm[r.c(i) * 8 + 7]);
         if constexpr (ADJ) {
             gs[o] = g[i];
             us[r.c(i) * H::RO + r.t(i)] = u[i];
@@ -779,60 +783,44 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
     }
 }
 
-// A of one lane's 4 states (times log2 e), zeros past dim or d_state. With A per head the
-// second pair holds what the product's rounding left: a head's dA sums over all its states and
-// channels, where an A off by 2^-25 shows (for single states it averages out).
-template <int S, bool HEADS>
-__device__ __forceinline__ void load_A(const BwdParams& p, const float* prm, int c, int d, int j, uint64_t (&A2)[2]) {
+// A of one lane's 4 states (times log2 e), zeros past dim or d_state.
+template <int S>
+__device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_t (&A2)[2]) {
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int n = 4 * j + (k ^ slot_order<S>(d));
-        const bool in = !HEADS && d < p.dim && n < p.dstate;
-        a[k] = in ? kLog2e * p.A[(int64_t)d * p.dstate + n] : 0.f;
+        a[k] = d < p.dim && n < p.dstate ? kLog2e * p.A[(int64_t)d * p.dstate + n] : 0.f;
     }
     A2[0] = pk2(a[0], a[1]);
     A2[1] = pk2(a[2], a[3]);
-    if constexpr (HEADS) {
-        constexpr float kLog2eRest = (float)(1.4426950408889634073599 - (double)kLog2e);
-        const float A = prm[c * 8 + 7];
-        const float hi = A * kLog2e, lo = fmaf(A, kLog2eRest, fmaf(A, kLog2e, -hi));
-        A2[0] = pk2(hi, hi);
-        A2[1] = pk2(lo, lo);
-    }
 }
 
-// Decay of one step for a lane's 4 states: 2^(delta A log2 e). With A per head one exp
-// serves all. d2: delta twice.
+// Decay of one step for a lane's 4 states: 2^(delta A log2 e). d2: delta twice.
 // The SFU's exp comes out low on average: by 5e-9 to 8e-9 of its value for exponents above
 // -0.003, by 1.3e-8 to 2.9e-8 from there to -1 (means over 4 M random arguments each). A state
 // that decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which showed in
-// dA (2.5e-6 of its norm at the 130M layer's sizes, where an unbiased exp leaves 4e-7). The
+// dA (2.5e-6 of its norm at the 130M layer's sizes, where an unbiased exp leaves 1.2e-6). The
 // exponent is therefore raised by the middle of that range, in the multiply that forms it.
 constexpr float kExpBias = 2.5e-8f;
-template <bool HEADS>
 __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint64_t (&a)[2]) {
-    if constexpr (HEADS) {
-        const float d = lo2(d2);
-        const float e = ex2(fmaf(d, lo2(A2[0]), fmaf(d, lo2(A2[1]), kExpBias)));
-        a[0] = a[1] = pk2(e, e);
-    } else {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 x = upk2(fma2(d2, A2[k], pk2(kExpBias, kExpBias)));
-            a[k] = pk2(ex2(x.x), ex2(x.y));
-        }
+    for (int k = 0; k < 2; ++k) {
+        const float2 x = upk2(fma2(d2, A2[k], pk2(kExpBias, kExpBias)));
+        a[k] = pk2(ex2(x.x), ex2(x.y));
     }
 }
 
 // Decays and delta u of the T steps from row, the decays zero at the sequence starts in mask.
+// With A per head the decays are staged (from as).
 template <bool HEADS, int T>
-__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, uint32_t mask,
+__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, const float* as, uint32_t mask,
                                        uint64_t (&a)[T][2], uint64_t (&du2)[T]) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         const float2 s = row[i];
-        decay<HEADS>(A2, pk2(s.x, s.x), a[i]);
+        if constexpr (HEADS) a[i][0] = a[i][1] = pk2(as[i], as[i]);
+        else decay(A2, pk2(s.x, s.x), a[i]);
         du2[i] = pk2(s.y, s.y);
     }
     if (mask) {
@@ -875,17 +863,19 @@ __device__ __forceinline__ int64_t ns_off(const BwdParams& p, int64_t row, int d
 template <int S> struct BwdStaged {
     using H = BwdShape<S>;
     float2* st;
-    float *gs, *us, *Bs, *Cs;
-    __device__ __forceinline__ BwdStaged(float* sm, bool adj) {
+    float *as, *gs, *us, *Bs, *Cs;
+    __device__ __forceinline__ BwdStaged(float* sm, bool adj, bool heads) {
         st = reinterpret_cast<float2*>(sm);
-        gs = sm + H::kSt;
-        us = sm + H::kSt + (adj ? H::kG : 0);
+        as = sm + H::kSt;
+        gs = as + (heads ? H::kDecay : 0);
+        us = gs + (adj ? H::kG : 0);
         Bs = us + (adj ? H::kU : 0);
         Cs = Bs + H::kBC;
     }
     __device__ __forceinline__ BwdStaged at(int n, int size) const {
         BwdStaged r = *this;
         r.st += n * size / 2;
+        r.as += n * size;
         r.gs += n * size;
         r.us += n * size;
         r.Bs += n * size;
@@ -901,8 +891,8 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
     constexpr bool SUM = MODE == kSummary;
     constexpr int KL = H::KL, ST = H::T;
     extern __shared__ __align__(16) float sm[];
-    constexpr int kStaged = H::kStaged(SUM);
-    const BwdStaged<S> staged(sm, SUM);
+    constexpr int kStaged = H::kStaged(SUM, HEADS);
+    const BwdStaged<S> staged(sm, SUM, HEADS);
     float* prm = sm + 2 * kStaged;
     uint32_t* mask = reinterpret_cast<uint32_t*>(prm + H::kPrm);
     uint8_t* raw = reinterpret_cast<uint8_t*>(prm + H::kPrm + H::kMask);
@@ -925,7 +915,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
         };
         auto stage = [&](int n) {
             const BwdStaged<S> to = staged.at(n & 1, kStaged);
-            stage_tile<T, S, CL, Q8, SUM>(p, hid, b, d0, tb + n * H::TT, raw + (n & 1) * kRaw, prm, to.st, to.gs,
+            stage_tile<T, S, CL, Q8, SUM, HEADS>(p, hid, b, d0, tb + n * H::TT, raw + (n & 1) * kRaw, prm, to.st, to.as, to.gs,
                                           to.us, to.Bs, to.Cs, mask + (n & 1));
         };
         if (p.async)                                           // a thread reads back its own entries
@@ -946,8 +936,8 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
     for (int kc = 0; kc < H::KC; ++kc)
 #pragma unroll
         for (int kl = 0; kl < KL; ++kl) {
-            const int c = H::channel(warp, kc, cl, j, kl), d = d0 + c;
-            load_A<S, HEADS>(p, prm, c, d, j, A2[kc][kl]);
+            const int d = d0 + H::channel(warp, kc, cl, j, kl);
+            if constexpr (!HEADS) load_A<S>(p, d, j, A2[kc][kl]);
             R[kc][kl][0] = R[kc][kl][1] = 0;
             P[kc][kl][0] = P[kc][kl][1] = pk2(1.f, 1.f);
             h[kc][kl][0] = h[kc][kl][1] = 0;
@@ -974,7 +964,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
                     so[kl] = c * (H::TT + 1) + sub * ST;
                     if (!SUM && d0 + c < p.dim)
                         stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / ST + sub, d0 + c, j), h[kc][kl]);
-                    decays<HEADS, ST>(A2[kc][kl], in.st + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
+                    decays<HEADS, ST>(A2[kc][kl], in.st + so[kl], in.as + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
                 }
 #pragma unroll
                 for (int i = 0; i < ST; ++i) {
@@ -1068,8 +1058,8 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
     constexpr int KC = H::KC, KL = H::KL, ST = H::T, TT = H::TT, E = H::EPT;
     constexpr bool REGS = KC == 1;                             // m and dA in registers, else carried over
     extern __shared__ __align__(16) float sm[];
-    constexpr int kStaged = H::kStaged(true);
-    const BwdStaged<S> staged(sm, true);
+    constexpr int kStaged = H::kStaged(true, HEADS);
+    const BwdStaged<S> staged(sm, true, HEADS);
     float* outs = sm + 2 * kStaged;                            // y, s1, s2 of two tiles
     float* part = outs + 6 * H::kOut;
     float* prm = part + H::kPart;
@@ -1105,7 +1095,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
         };
         auto stage = [&](int n) {
             const BwdStaged<S> to = staged.at(n & 1, kStaged);
-            stage_tile<T, S, CL, Q8, true>(p, hid, b, d0, start(n), raw + n % 3 * kRaw, prm, to.st, to.gs, to.us,
+            stage_tile<T, S, CL, Q8, true, HEADS>(p, hid, b, d0, start(n), raw + n % 3 * kRaw, prm, to.st, to.as, to.gs, to.us,
                                            to.Bs, to.Cs, mask + (n & 1));
         };
         // the gradients of a tile, one run per thread
@@ -1119,7 +1109,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
             const int pos = p.reverse ? L - 1 - t : t;
             const int hi = CL ? (t < L ? min(E, p.dim - d) : 0) : (d < p.dim ? min(E, L - t) : 0);
             if (hi > 0) {
-                float dt[E], z[E], dy[E], du[E], ddt[E], dz[E];
+                float dt[E], z[E], dy[E], du[E], ddt[E], dz[E], tileD = 0.f, tileBias = 0.f;
                 take<T, S, CL, Q8>(p, from, 1, run, t0, dt);
                 if (p.z.p) {
                     take<T, S, CL, Q8>(p, from, 2, run, t0, z);
@@ -1131,7 +1121,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                     const float2 s = in.st[c * (TT + 1) + tl];
                     const float g = in.gs[c * (TT + 1) + tl];
                     const float u = in.us[o], Dv = prm[c * 8 + 6];
-                    const float s1 = s1s[o], s2 = s2s[o] * kLn2;
+                    const float s1 = s1s[o], s2 = s2s[o] * (HEADS ? prm[c * 8 + 7] : kLn2);
                     du[i] = fmaf(g, Dv, s.x * s1);
                     const float ddelta = fmaf(u, s1, s2);
                     ddt[i] = p.softplus ? ddelta * sigmoidf_(dt[i] + prm[c * 8 + 5]) : ddelta;
@@ -1145,10 +1135,12 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                             sums[H::G * TT + c * TT + tl] += ddt[i];
                         }
                     } else if (i < hi) {
-                        dD = fmaf(g, u, dD);
-                        dBias += ddt[i];
+                        tileD = fmaf(g, u, tileD);             // the run first: fewer roundings of
+                        tileBias += ddt[i];                    // the long sum
                     }
                 }
+                dD += tileD;
+                dBias += tileBias;
                 if constexpr (CL) {
                     auto at = [&](const Str& s) { return (int64_t)b * s.b + d + (int64_t)pos * s.p; };
                     if (p.du32) put_run<float, E>(p.du32 + at(p.sdu), false, p.vec_out, hi, du);
@@ -1222,7 +1214,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
             if (te == L) load_state<S>(p, p.dhl, b, d, j, m[kl]);
             else if (d < p.dim) ldpair(p.sumR + ns_off<S>(p, row, d, j), m[kl]);
             if constexpr (REGS) {
-                load_A<S, HEADS>(p, prm, d - d0, d, j, A2[kl]);
+                if constexpr (!HEADS) load_A<S>(p, d, j, A2[kl]);
             } else {
                 stpair(place(kc, kl), m[kl]);
                 stpair(place(kc, kl) + 4, dA[kl]);
@@ -1306,7 +1298,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                     const int c = H::channel(warp, kc, cl, j, kl);
                     so[kl] = c * (TT + 1) + sub * ST;
                     if constexpr (!REGS) {
-                        load_A<S, HEADS>(p, prm, c, d0 + c, j, A2[kl]);
+                        if constexpr (!HEADS) load_A<S>(p, d0 + c, j, A2[kl]);
                         ldpair(place(kc, kl), m[kl]);
                         ldpair(place(kc, kl) + 4, dA[kl]);
                     }
@@ -1318,7 +1310,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                     uint64_t du2[KL][ST];
 #pragma unroll
                     for (int kl = 0; kl < KL; ++kl)
-                        decays<HEADS, ST>(A2[kl], st + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
+                        decays<HEADS, ST>(A2[kl], st + so[kl], in.as + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
 #pragma unroll
                     for (int i = 0; i < ST; ++i) {
                         uint64_t bv[2];
@@ -1359,7 +1351,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                         s1[v] = f1.x + f1.y;
                         if constexpr (HEADS) {
                             const float2 f2 = upk2(add2(q[0], q[1]));
-                            s2[v] = lo2(A2[kl][0]) * (f2.x + f2.y);
+                            s2[v] = f2.x + f2.y;                // times A: see finish()
                         } else {
                             const float2 f2 = upk2(fma2(q[1], A2[kl][1], mul2(q[0], A2[kl][0])));
                             s2[v] = f2.x + f2.y;

@@ -24,16 +24,16 @@ inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t 
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid, H::NT,
-                                2 * H::kStaged(false) * 4 + kHead + 2 * kRaw +
+                                2 * H::kStaged(false, HEADS) * 4 + kHead + 2 * kRaw +
                                     BwdCopies<T, S, CL, Q8, false>::COUNT * 16,
                                 p, st);
     if (what == 1)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kSummary>, grid, H::NT,
-                                2 * H::kStaged(true) * 4 + kHead + 2 * kRaw +
+                                2 * H::kStaged(true, HEADS) * 4 + kHead + 2 * kRaw +
                                     BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                                 p, st);
     return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid, H::NT,
-                            (2 * H::kStaged(true) + 6 * H::kOut + H::kPart + H::kCarry + (CL ? H::kSum : 0)) * 4 +
+                            (2 * H::kStaged(true, HEADS) + 6 * H::kOut + H::kPart + H::kCarry + (CL ? H::kSum : 0)) * 4 +
                                 kHead + 3 * kRaw + BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                             p, st);
 }

@@ -2,6 +2,8 @@
 checked here (ValueError / TypeError), sizes and pointers in the library (SSMError)."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _abi
@@ -13,6 +15,18 @@ def dtype_code(t, name="activations"):
     if t.dtype not in DTYPES:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
     return DTYPES[t.dtype]
+
+
+def on_stream(fn):
+    """Run a call that is given a stream with that stream current, so that what it allocates
+    (outputs, workspace) belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, stream=stream, **kw)
+    return call
 
 
 class Call:

@@ -10,7 +10,7 @@ import ctypes
 import torch
 
 from . import _abi
-from ._marshal import Call, dtype_code
+from ._marshal import Call, dtype_code, on_stream
 
 __all__ = ["ssm_state_cache_write", "ssm_state_cache_read", "ssm_selective_state_update_cached"]
 
@@ -28,6 +28,7 @@ def _cache(call, codes, scales, slots, rand, batch):
             call.ptr(rand, "rand", (batch, dim), rand.dtype if rand is not None else None))
 
 
+@on_stream
 def ssm_state_cache_write(state, codes, scales, *, slots=None, rand=None, stream=None):
     """Write fp32 states (batch, dim, dstate) into their slots of the cache."""
     call = Call(codes)
@@ -40,6 +41,7 @@ def ssm_state_cache_write(state, codes, scales, *, slots=None, rand=None, stream
               n, num_slots), stream)
 
 
+@on_stream
 def ssm_state_cache_read(codes, scales, *, slots=None, dtype=torch.float32, out=None, stream=None):
     """The states of the slots, (batch, dim, dstate) in ``dtype`` (or into ``out``, whose rows
     without a slot keep what they hold; a new tensor has zeros there)."""
@@ -57,6 +59,7 @@ def ssm_state_cache_read(codes, scales, *, slots=None, dtype=torch.float32, out=
     return out
 
 
+@on_stream
 def ssm_selective_state_update_cached(codes, scales, conv_state, x, dt, A, B, C, D=None, z=None,
                                       dt_bias=None, dt_softplus=True, conv_weight=None,
                                       conv_bias=None, *, slots=None, rand=None, out=None,

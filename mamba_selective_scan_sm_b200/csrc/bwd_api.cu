@@ -211,6 +211,10 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         return api_fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", pl.total,
                         a->workspace ? a->workspace_bytes : (size_t)0);
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
+    for (const Arg& o : outs)                                  // views may interleave, not coincide
+        for (const Arg& q : outs)
+            if (&o < &q && o.p && o.p == q.p && o.bytes && q.bytes)
+                return api_fail(SSM_ERR_ALIAS, "%s and %s are the same", o.name, q.name);
     for (const Arg& o : outs)                                  // the last is the workspace itself
         if (&o != std::end(outs) - 1 && ranges_overlap(a->workspace, pl.total, o.p, o.bytes))
             return api_fail(SSM_ERR_ALIAS, "%s overlaps workspace", o.name);

@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _abi
-from ._marshal import DTYPES, Call, dtype_code
+from ._marshal import DTYPES, Call, dtype_code, on_stream
 
 __all__ = ["ScanGrads", "ConvGrads", "Packed8", "ssm_selective_scan_bwd",
            "ssm_selective_scan_bwd_workspace_size", "ssm_causal_conv1d_bwd",
@@ -85,6 +85,7 @@ def ssm_selective_scan_bwd_workspace_size(batch, dim, seqlen, dstate, dtype=torc
                            int(bool(packed_sequences)), int(bool(channel_last)), num_segments)
 
 
+@on_stream
 def ssm_selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None,
                            delta_softplus=True, reverse=False, conv_weight=None, conv_bias=None, *,
                            dfinal_state=None, initial_state=None, conv_history=None,
@@ -200,6 +201,7 @@ def ssm_selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=N
     return g
 
 
+@on_stream
 def ssm_causal_conv1d_bwd(dout, x, w, bias=None, apply_silu=True, *, workspace=None, stream=None):
     """Gradients of ``ssm_causal_conv1d_fwd(x, w, bias, apply_silu)`` for the gradient
     ``dout`` of its output. Returns ``ConvGrads(dx, dw, dbias)``."""
@@ -227,6 +229,7 @@ def ssm_causal_conv1d_bwd(dout, x, w, bias=None, apply_silu=True, *, workspace=N
     return ConvGrads(dx, dw, db)
 
 
+@on_stream
 def ssm_checkpoint_pack(x, *, channel_last=False, codes=None, scales=None, stream=None):
     """Pack an activation into 8 bits: x (batch, dim, seqlen), or channel-last (batch,
     seqlen, dim), possibly a view with a position stride. Per channel and 64 positions,
@@ -255,6 +258,7 @@ def ssm_checkpoint_pack(x, *, channel_last=False, codes=None, scales=None, strea
     return Packed8(codes, scales)
 
 
+@on_stream
 def ssm_checkpoint_unpack(packed, dtype=torch.bfloat16, *, channel_last=False, out=None, stream=None):
     """Read a ``Packed8`` back as a dense tensor of ``dtype`` (or into ``out``)."""
     codes, scales = packed

@@ -68,7 +68,7 @@ CASES = [
     (dict(workspace=P + 8), "SSM_ERR_MISALIGNED"), (dict(workspace=None), "SSM_ERR_WORKSPACE"),
     (dict(workspace_bytes=100), "SSM_ERR_WORKSPACE"), (dict(du=FAKE), "SSM_ERR_ALIAS"),
     (dict(dB=FAKE + (3 << 28)), "SSM_ERR_ALIAS"), (dict(workspace=FAKE), "SSM_ERR_ALIAS"),
-    (dict(dC=FAKE + (11 << 28)), "SSM_ERR_ALIAS"),
+    (dict(dC=FAKE + (11 << 28)), "SSM_ERR_ALIAS"), (dict(ddelta=FAKE + (6 << 28)), "SSM_ERR_ALIAS"),
 ]
 
 

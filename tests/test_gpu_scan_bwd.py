@@ -231,6 +231,28 @@ def test_same_bits_every_time_and_on_another_stream():
             assert torch.equal(v, getattr(b, k)), k
 
 
+def test_a_given_stream_owns_what_the_call_allocates():
+    """stream=: workspaces and outputs come from that stream's memory, so that work queued on the
+    current stream right after the call cannot take them over."""
+    m = ssm()
+    c = case(27, "f32", 2, 64, 200, 16, conv=4)
+    f = lambda k: gpu(c[k], "f32")  # noqa: E731
+    args = (f("dout"), f("u"), f("delta"), f("A"), f("B"), f("C"), f("D"), f("z"), f("delta_bias"), True, False,
+            f("conv_w"), f("conv_b"))
+    want = m.ssm_selective_scan_bwd(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = m.ssm_selective_scan_bwd(*args, stream=side)
+        junk = [torch.full((1 << 18,), float("nan"), device="cuda") for _ in range(40)]
+        del junk
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got) if x is not None)
+    kept = m.ssm_checkpoint_pack(f("u"), stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(kept.codes, m.ssm_checkpoint_pack(f("u")).codes)
+
+
 def test_two_calls_at_once_and_a_graph():
     """Calls on two streams with workspaces of their own, and a captured call replayed on new
     inputs, give what plain calls give."""

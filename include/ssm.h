@@ -396,7 +396,7 @@ SSM_API ssm_status_t ssm_causal_conv1d_bwd_workspace_size(int64_t batch, int64_t
 /*
  * Gradients of ssm_causal_conv1d_fwd: dx (batch, dim, seqlen) in dtype, dw (dim, width)
  * and dbias (dim) fp32 (either of the two may be NULL), from its inputs and dout (batch,
- * dim, seqlen) in dtype. dx must not overlap x or dout (SSM_ERR_ALIAS).
+ * dim, seqlen) in dtype. No output may overlap an input or another (SSM_ERR_ALIAS).
  */
 SSM_API ssm_status_t ssm_causal_conv1d_bwd(const void* dout, const void* x, const float* w,
                                            const float* bias, void* dx, float* dw, float* dbias,
@@ -473,9 +473,9 @@ typedef struct {
 /* The decode step of ssm_selective_state_update_ex on a cache: reads the row's state from
  * its slot, takes one step in fp32, gives out from the new state before it is rounded, and
  * writes the state back in 8 bits (a quotient within 1e-4 of a border between two codes may
- * take either: the new state's own fp32 rounding is of that size). conv_state is held per slot too. Errors as there;
- * SSM_ERR_BAD_SHAPE also for num_slots < batch without slots, batch * dim from 2^31 and
- * num_slots * dim from 2^32 on. */
+ * take either: the new state's own fp32 rounding is of that size). conv_state is held per
+ * slot too. Errors as there; SSM_ERR_BAD_SHAPE also for num_slots < batch without slots,
+ * batch * dim from 2^31 and num_slots * dim from 2^32 on. */
 SSM_API ssm_status_t ssm_selective_state_update_cached(const ssm_cached_update_args_t* args,
                                                        ssm_stream_t stream);
 

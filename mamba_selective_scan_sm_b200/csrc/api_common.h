@@ -40,10 +40,12 @@ inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 // A pointer argument: its alignment, and the bytes it spans (0 where they are not checked).
+// Views in rows: row bytes every step bytes.
 struct Arg {
     const void* p;
     size_t align, bytes;
     const char* name;
+    size_t row = 0, step = 0;
 };
 
 template <int N>
@@ -60,6 +62,23 @@ inline ssm_status_t check_alias(const Arg (&outs)[NO], const Arg (&ins)[NI]) {
         for (const Arg& i : ins)
             if (ranges_overlap(o.p, o.bytes, i.p, i.bytes))
                 return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", o.name, i.name);
+    return SSM_OK;
+}
+
+// Two outputs may interleave (columns of one tensor) but not share an element.
+template <int N>
+inline ssm_status_t check_distinct(const Arg (&outs)[N]) {
+    for (int i = 0; i < N; ++i)
+        for (int k = 0; k < i; ++k) {
+            const bool later = reinterpret_cast<uintptr_t>(outs[i].p) >= reinterpret_cast<uintptr_t>(outs[k].p);
+            const Arg &x = later ? outs[i] : outs[k], &y = later ? outs[k] : outs[i];
+            if (!ranges_overlap(x.p, x.bytes, y.p, y.bytes)) continue;
+            if (x.step != 0 && x.step == y.step) {             // x's first row among y's rows
+                const size_t d = (reinterpret_cast<uintptr_t>(x.p) - reinterpret_cast<uintptr_t>(y.p)) % x.step;
+                if (d >= y.row && x.step - d >= x.row) continue;
+            }
+            return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
+        }
     return SSM_OK;
 }
 

@@ -1,7 +1,6 @@
 // C ABI of the gradients (include/ssm.h): argument checks, the workspace's layout and the
 // launches of a backward pass. Nothing here allocates, frees or synchronises.
 #include <algorithm>
-#include <iterator>
 
 #include "api_common.h"
 #include "bwd_launch.h"
@@ -188,11 +187,14 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         {a->seq_starts, 4, a->seq_starts ? ((size_t)a->num_seqs + 1) * 4 : 0, "seq_starts"},
         {a->u_scale, 4, sc_bytes, "u_scale"}, {a->delta_scale, 4, sc_bytes, "delta_scale"},
         {a->z_scale, 4, sc_bytes, "z_scale"}};
+    auto rows_out = [&](const void* q, int64_t st, int64_t width, const char* name) {
+        return cl ? Arg{q, es, span(st, width, es), name, (size_t)width * es, (size_t)(st ? st : width) * es}
+                  : Arg{q, es, span(st, width, es), name};
+    };
     const Arg outs[] = {
-        {a->du, es, span(a->stride_du, D, es), "du"},
-        {a->ddelta, es, span(a->stride_ddelta, D, es), "ddelta"},
-        {a->dz, es, span(a->stride_dz, D, es), "dz"},
-        {a->dB, es, span(a->stride_dB, N, es), "dB"}, {a->dC, es, span(a->stride_dC, N, es), "dC"},
+        rows_out(a->du, a->stride_du, D, "du"), rows_out(a->ddelta, a->stride_ddelta, D, "ddelta"),
+        rows_out(a->dz, a->stride_dz, D, "dz"), rows_out(a->dB, a->stride_dB, N, "dB"),
+        rows_out(a->dC, a->stride_dC, N, "dC"),
         {a->dA, 4, a_bytes, "dA"}, {a->dD, 4, (size_t)D * 4, "dD"},
         {a->ddelta_bias, 4, (size_t)D * 4, "ddelta_bias"},
         {a->dconv_weight, 4, w_bytes, "dconv_weight"}, {a->dconv_bias, 4, (size_t)D * 4, "dconv_bias"},
@@ -211,13 +213,7 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         return api_fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", pl.total,
                         a->workspace ? a->workspace_bytes : (size_t)0);
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
-    for (const Arg& o : outs)                                  // views may interleave, not coincide
-        for (const Arg& q : outs)
-            if (&o < &q && o.p && o.p == q.p && o.bytes && q.bytes)
-                return api_fail(SSM_ERR_ALIAS, "%s and %s are the same", o.name, q.name);
-    for (const Arg& o : outs)                                  // the last is the workspace itself
-        if (&o != std::end(outs) - 1 && ranges_overlap(a->workspace, pl.total, o.p, o.bytes))
-            return api_fail(SSM_ERR_ALIAS, "%s overlaps workspace", o.name);
+    if ((status = check_distinct(outs)) != SSM_OK) return status;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -439,9 +435,7 @@ ssm_status_t ssm_causal_conv1d_bwd(const void* dout, const void* x, const float*
         return api_fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                         workspace ? workspace_bytes : (size_t)0);
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
-    for (int i = 0; i < 3; ++i)
-        if (ranges_overlap(outs[3].p, need, outs[i].p, outs[i].bytes))
-            return api_fail(SSM_ERR_ALIAS, "%s overlaps workspace", outs[i].name);
+    if ((status = check_distinct(outs)) != SSM_OK) return status;
     const Str str{dim * seqlen, seqlen, 1};
     ConvBwdParams c{};
     c.batch = (int)batch;

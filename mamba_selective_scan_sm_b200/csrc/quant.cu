@@ -168,8 +168,7 @@ ssm_status_t ssm_checkpoint_pack(const void* x, void* codes, float* scales, int6
     if ((status = check_aligned(ins)) != SSM_OK) return status;
     if ((status = check_aligned(outs)) != SSM_OK) return status;
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
-    if (ranges_overlap(outs[0].p, outs[0].bytes, outs[1].p, outs[1].bytes))
-        return api_fail(SSM_ERR_ALIAS, "codes overlaps scales");
+    if ((status = check_distinct(outs)) != SSM_OK) return status;
     PackParams p{x, sx, static_cast<int8_t*>(codes), scales, nullptr, (int)batch, (int)dim, (int)seqlen,
                  is_aligned(x, 16) && sx % 8 == 0};
     cudaError_t e = launch_pack((int)es, channel_last != 0, p, static_cast<cudaStream_t>(stream));
@@ -212,8 +211,7 @@ ssm_status_t ssm_state_cache_write(const float* state, void* codes, float* scale
     if ((status = check_aligned(ins)) != SSM_OK) return status;
     if ((status = check_aligned(outs)) != SSM_OK) return status;
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
-    if (ranges_overlap(codes, held * dstate, scales, held * 4))
-        return api_fail(SSM_ERR_ALIAS, "codes overlaps scales");
+    if ((status = check_distinct(outs)) != SSM_OK) return status;
     CacheParams p{};
     p.batch = batch;
     p.dim = dim;
@@ -296,10 +294,7 @@ ssm_status_t ssm_selective_state_update_cached(const ssm_cached_update_args_t* a
     if ((status = check_aligned(ins)) != SSM_OK) return status;
     if ((status = check_aligned(outs)) != SSM_OK) return status;
     if ((status = check_alias(outs, ins)) != SSM_OK) return status;
-    for (int i = 0; i < 4; ++i)
-        for (int k = 0; k < i; ++k)
-            if (ranges_overlap(outs[i].p, outs[i].bytes, outs[k].p, outs[k].bytes))
-                return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
+    if ((status = check_distinct(outs)) != SSM_OK) return status;
     CacheParams p{};
     p.batch = a->batch;
     p.dim = a->dim;

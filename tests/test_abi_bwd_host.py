@@ -69,6 +69,11 @@ CASES = [
     (dict(workspace_bytes=100), "SSM_ERR_WORKSPACE"), (dict(du=FAKE), "SSM_ERR_ALIAS"),
     (dict(dB=FAKE + (3 << 28)), "SSM_ERR_ALIAS"), (dict(workspace=FAKE), "SSM_ERR_ALIAS"),
     (dict(dC=FAKE + (11 << 28)), "SSM_ERR_ALIAS"), (dict(ddelta=FAKE + (6 << 28)), "SSM_ERR_ALIAS"),
+    # outputs that share some elements, dense or as columns of one tensor
+    (dict(ddelta=FAKE + (6 << 28) + 64), "SSM_ERR_ALIAS"), (dict(dA=FAKE + (6 << 28) + 128), "SSM_ERR_ALIAS"),
+    (dict(channel_last=1, stride_du=160, stride_ddelta=160, ddelta=FAKE + (6 << 28) + 126), "SSM_ERR_ALIAS"),
+    (dict(channel_last=1, stride_du=160, stride_ddelta=160, ddelta=FAKE + (6 << 28) + 194), "SSM_ERR_ALIAS"),
+    (dict(channel_last=1, stride_du=160, stride_ddelta=128, ddelta=FAKE + (6 << 28) + 128), "SSM_ERR_ALIAS"),
 ]
 
 
@@ -108,7 +113,8 @@ def test_workspace_sizes(lib):
     (dict(dtype=9), "SSM_ERR_BAD_DTYPE"), (dict(width=5), "SSM_ERR_BAD_SHAPE"), (dict(batch=-2), "SSM_ERR_BAD_SHAPE"),
     (dict(dout=None), "SSM_ERR_NULL_ARG"), (dict(dx=None), "SSM_ERR_NULL_ARG"), (dict(ws=None), "SSM_ERR_WORKSPACE"),
     (dict(ws_bytes=8), "SSM_ERR_WORKSPACE"), (dict(dx=FAKE), "SSM_ERR_ALIAS"), (dict(dx=FAKE + 1), "SSM_ERR_MISALIGNED"),
-    (dict(dim=1 << 29, batch=1 << 20), "SSM_ERR_BAD_SHAPE"),
+    (dict(dim=1 << 29, batch=1 << 20), "SSM_ERR_BAD_SHAPE"), (dict(dbias=FAKE + (4 << 28) + 64), "SSM_ERR_ALIAS"),
+    (dict(dw=FAKE + (5 << 28)), "SSM_ERR_ALIAS"),
 ])
 def test_conv_bwd_refusals(lib, kw, status):
     v = dict(dout=FAKE, x=FAKE + (1 << 28), w=FAKE + (2 << 28), bias=None, dx=FAKE + (3 << 28), dw=FAKE + (4 << 28),

@@ -157,7 +157,7 @@ int conv_bwd_chunk(bool channel_last) { return channel_last ? kConvClChunk : kCo
 cudaError_t launch_conv_bwd(int elem_size, bool channel_last, const ConvBwdParams& p, cudaStream_t st) {
     if (channel_last) {
         const int per = 128 * kConvClRun;
-        const dim3 g((p.dim + per - 1) / per, p.batch, p.chunks);
+        const dim3 g((unsigned)((p.dim + per - 1) / per) * (unsigned)p.chunks, p.batch);
         const bool q8 = p.x.scale != nullptr;
         if (elem_size == 2) {
             if (q8) conv_bwd_cl_kernel<__nv_bfloat16, true><<<g, 128, 0, st>>>(p);

@@ -196,8 +196,10 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
     constexpr int E = kConvClRun, U = kConvClAhead;
     using X = std::conditional_t<Q8, int8_t, T>;
     const int L = p.seqlen;
-    const int d = (blockIdx.x * blockDim.x + threadIdx.x) * E;
-    const int b = blockIdx.y, chunk = blockIdx.z;
+    // groups of channels times chunks of steps along x: both may pass 65535
+    const int groups = (p.dim + 128 * E - 1) / (128 * E);
+    const int chunk = blockIdx.x / groups, b = blockIdx.y;
+    const int d = ((blockIdx.x - chunk * groups) * 128 + threadIdx.x) * E;
     if (d >= p.dim) return;
     const int hi = min(E, p.dim - d);
     const int tb = chunk * p.chunk_len, te = min(L, tb + p.chunk_len);

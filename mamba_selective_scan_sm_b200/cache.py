@@ -86,6 +86,8 @@ def ssm_selective_state_update_cached(codes, scales, conv_state, x, dt, A, B, C,
     a.dt_bias, a.dt_softplus = call.ptr(dt_bias, "dt_bias", (dim,), f32), int(bool(dt_softplus))
     if conv_weight is not None:
         width = conv_weight.shape[-1]
+        if width < 1:
+            raise ValueError("conv_weight has no taps")
         a.conv_weight, a.conv_width = call.ptr(conv_weight, "conv_weight", (dim, width), f32), width
         a.conv_bias = call.ptr(conv_bias, "conv_bias", (dim,), f32)
         if conv_state is None:

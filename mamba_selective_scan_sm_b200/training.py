@@ -148,6 +148,8 @@ def ssm_selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=N
     width = 0
     if conv_weight is not None:
         width = conv_weight.shape[-1]
+        if width < 1:
+            raise ValueError("conv_weight has no taps")
         a.conv_weight, a.conv_width = call.ptr(conv_weight, "conv_weight", (dim, width), f32), width
         a.conv_bias = call.ptr(conv_bias, "conv_bias", (dim,), f32)
     elif conv_bias is not None or conv_history is not None:

@@ -201,6 +201,27 @@ def test_strided_views():
     assert torch.all(dxz[..., 2 * D:] == 7.0) and torch.all(dbc[..., :3] == 7.0)
 
 
+def test_rows_of_more_steps_than_a_grid_axis_holds_chunks():
+    """Either layout of one row of 2^22 + 100 steps, whose conv's gradient takes more than
+    65535 chunks channel-last. Inputs within 1 and decays below 0.86 (7 steps of memory): a
+    value collects 7 * 2^-22 of terms at most some ten times the rms, in both calls: 4e-5. The
+    sums over all steps: 2^22 terms below 10, whose partial sums stay near 10 sqrt(L), rounded
+    at random: 2^-24 * 10 L, 2.5; their own 2e-6 each the same way, less. 1e-2 sqrt(L) is 20."""
+    B, D, L, N = 1, 3, (1 << 22) + 100, 1
+    r = torch.Generator(device="cuda").manual_seed(5)
+    f = lambda *s: 2 * torch.rand(*s, device="cuda", generator=r) - 1  # noqa: E731
+    u, delta, dout, b, c, w = f(B, D, L), f(B, D, L), f(B, D, L), f(B, N, L), f(B, N, L), f(D, 4) / 2
+    A = -torch.rand(D, N, device="cuda", generator=r) - 0.5
+    t = lambda x: x.transpose(1, 2).contiguous()  # noqa: E731
+    a = ssm().ssm_selective_scan_bwd(dout, u, delta, A, b, c, conv_weight=w)
+    g = ssm().ssm_selective_scan_bwd(t(dout), t(u), t(delta), A, t(b), t(c), conv_weight=w, channel_last=True)
+    for k in ("du", "ddelta", "dB", "dC"):
+        check(k, host(getattr(g, k), True), host(getattr(a, k)), "f32")
+    for k in ("dA", "dconv_weight"):
+        want = host(getattr(a, k))
+        assert np.all(np.abs(host(getattr(g, k)) - want) <= 1e-2 * np.sqrt(L)), k
+
+
 def test_misaligned_rows():
     """Rows whose length and base are not multiples of 16 bytes take the scalar loads."""
     c = case(11, "bf16", 2, 33, 61, 16, conv=4)
@@ -385,3 +406,18 @@ def test_refusals():
     with pytest.raises(m.SSMError) as e:
         m.ssm_selective_scan_bwd(*ok, du=t["u"])
     assert e.value.name == "SSM_ERR_ALIAS"
+
+
+def test_a_conv_of_no_taps_is_refused():
+    """An empty weight has no address: it must not read as a call without a conv."""
+    m = ssm()
+    c = case(24, "f32", 1, 8, 10, 16)
+    t = {k: gpu(v, "f32") for k, v in c.items() if v is not None}
+    none = torch.zeros(8, 0, device="cuda")
+    with pytest.raises(ValueError):
+        m.ssm_selective_scan_bwd(t["dout"], t["u"], t["delta"], t["A"], t["B"], t["C"], conv_weight=none)
+    with pytest.raises(ValueError):
+        m.ssm_selective_state_update_cached(
+            torch.zeros(1, 8, 16, dtype=torch.int8, device="cuda"), torch.zeros(1, 8, device="cuda"),
+            torch.zeros(1, 8, 0, device="cuda"), t["u"][:, :, 0].contiguous(), t["u"][:, :, 0].contiguous(),
+            t["A"], t["B"][:, :, 0].contiguous(), t["C"][:, :, 0].contiguous(), conv_weight=none)

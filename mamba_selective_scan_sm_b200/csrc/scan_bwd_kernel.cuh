@@ -811,10 +811,9 @@ __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint
     }
 }
 
-// Decays and delta u of the T steps from row, the decays zero at the sequence starts in mask.
-// With A per head the decays are staged (from as).
+// Decays and delta u of the T steps from row. With A per head the decays are staged (from as).
 template <bool HEADS, int T>
-__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, const float* as, uint32_t mask,
+__device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, const float* as,
                                        uint64_t (&a)[T][2], uint64_t (&du2)[T]) {
 #pragma unroll
     for (int i = 0; i < T; ++i) {
@@ -823,12 +822,18 @@ __device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* ro
         else decay(A2, pk2(s.x, s.x), a[i]);
         du2[i] = pk2(s.y, s.y);
     }
-    if (mask) {
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-            if (mask >> i & 1) a[i][0] = a[i][1] = 0;
-    }
 }
+
+// The sequence starts among the T steps of a sub-tile, bit i for step i. Nothing passes a start
+// in either direction, not even a NaN, so zero decays would not do: a sub-tile that holds a
+// start is worked out with a test at each step, all others without one.
+template <int T> __device__ __forceinline__ uint32_t starts_in(uint32_t mask, int sub) {
+    return mask >> (sub * T) & ((1u << T) - 1);
+}
+// A segment's product of decays that holds a start: no product of decays, which are not
+// negative, comes out as this.
+constexpr float kCut = -0.f;
+__device__ __forceinline__ bool is_cut(float product) { return __float_as_uint(product) == 0x80000000u; }
 
 __device__ __forceinline__ void ldpair(const float* s, uint64_t (&v)[2]) {
     const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(s);
@@ -945,10 +950,11 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
             if (!SUM && seg > 0 && d < p.dim) ldpair(p.sumS + ns_off<S>(p, row, d, j), h[kc][kl]);
         }
     __syncthreads();                                           // tile 0 is staged
+    bool alive = true;                                         // no start in the segment so far
     for (int n = 0; n < ntiles; ++n) {
         const int t0 = tb + n * H::TT;
         const BwdStaged<S> in = staged.at(n & 1, kStaged);
-        const uint32_t starts = mask[n & 1];
+        const uint32_t starts = HEADS ? 0 : mask[n & 1];       // (not with A per head)
 #pragma unroll
         for (int kc = 0; kc < H::KC; ++kc) {
             const int q = slot_order<S>(H::channel(warp, kc, cl, 0, 0));
@@ -964,29 +970,51 @@ __global__ void __launch_bounds__(BwdShape<S>::NT) scan_bwd_states_kernel(const 
                     so[kl] = c * (H::TT + 1) + sub * ST;
                     if (!SUM && d0 + c < p.dim)
                         stpair(p.ckpt + ns_off<S>(p, (int64_t)b * p.nsub + t0 / ST + sub, d0 + c, j), h[kc][kl]);
-                    decays<HEADS, ST>(A2[kc][kl], in.st + so[kl], in.as + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
+                    decays<HEADS, ST>(A2[kc][kl], in.st + so[kl], in.as + so[kl], a[kl], du2[kl]);
                 }
+                const uint32_t cuts = starts_in<ST>(starts, sub);
+                bool on = alive && (starts & ((1u << sub * ST) - 1)) == 0;
+                auto steps = [&](auto cutting, auto summing) {
+                    constexpr bool CUT = decltype(cutting)::value, ADD = decltype(summing)::value;
 #pragma unroll
-                for (int i = 0; i < ST; ++i) {
-                    uint64_t bv[2], cv[2];
-                    ldpair(Br + i * H::RB, bv);
-                    if (SUM) ldpair(Cr + i * H::RB, cv);
+                    for (int i = 0; i < ST; ++i) {
+                        if (CUT && (cuts >> i & 1)) {
+                            on = false;
 #pragma unroll
-                    for (int kl = 0; kl < KL; ++kl) {
-                        uint64_t g2 = 0;
-                        if (SUM) g2 = pk2(in.gs[so[kl] + i], in.gs[so[kl] + i]);
+                            for (int kl = 0; kl < KL; ++kl) {
+                                h[kc][kl][0] = h[kc][kl][1] = 0;
+                                P[kc][kl][0] = P[kc][kl][1] = pk2(kCut, kCut);
+                            }
+                        }
+                        uint64_t bv[2], cv[2];
+                        ldpair(Br + i * H::RB, bv);
+                        if (ADD) ldpair(Cr + i * H::RB, cv);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            h[kc][kl][k] = fma2(a[kl][i][k], h[kc][kl][k], mul2(du2[kl][i], bv[k]));
-                            if (SUM) {
-                                P[kc][kl][k] = mul2(P[kc][kl][k], a[kl][i][k]);
-                                R[kc][kl][k] = fma2(P[kc][kl][k], mul2(g2, cv[k]), R[kc][kl][k]);
+                        for (int kl = 0; kl < KL; ++kl) {
+                            uint64_t g2 = 0;
+                            if (ADD) g2 = pk2(in.gs[so[kl] + i], in.gs[so[kl] + i]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                h[kc][kl][k] = fma2(a[kl][i][k], h[kc][kl][k], mul2(du2[kl][i], bv[k]));
+                                if (ADD && (!CUT || on)) {
+                                    P[kc][kl][k] = mul2(P[kc][kl][k], a[kl][i][k]);
+                                    R[kc][kl][k] = fma2(P[kc][kl][k], mul2(g2, cv[k]), R[kc][kl][k]);
+                                }
                             }
                         }
                     }
+                };
+                std::bool_constant<SUM> sums;
+                if constexpr (HEADS) {
+                    steps(std::false_type{}, sums);
+                } else {
+                    if (cuts) steps(std::true_type{}, sums);
+                    else if (SUM && !on) steps(std::false_type{}, std::false_type{});
+                    else steps(std::false_type{}, sums);
                 }
             }
         }
+        alive = alive && starts == 0;
         __syncthreads();                                       // tile n is done, n + 1 staged
     }
     if (SUM) {
@@ -1031,7 +1059,7 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
         for (int k = 0; k < U; ++k)
             if (s0 + k < p.nseg) {
                 Sx[(s0 + k) * per] = h;
-                h = fmaf(pr[k], h, e[k]);
+                h = is_cut(pr[k]) ? e[k] : fmaf(pr[k], h, e[k]);
             }
     }
     for (int s0 = p.nseg - 1; s0 >= 0; s0 -= U) {
@@ -1046,7 +1074,7 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
         for (int k = 0; k < U; ++k)
             if (s0 - k >= 0) {
                 Rx[(s0 - k) * per] = m;
-                m = fmaf(pr[k], m, r[k]);
+                m = is_cut(pr[k]) ? r[k] : fmaf(pr[k], m, r[k]);
             }
     }
 }
@@ -1268,7 +1296,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
         const float *Bs = in.Bs, *Cs = in.Cs;
         float* ys = outs + (n & 1) * 3 * H::kOut;
         float *s1s = ys + H::kOut, *s2s = s1s + H::kOut;
-        const uint32_t starts = mask[n & 1];
+        const uint32_t starts = HEADS ? 0 : mask[n & 1];
 #pragma unroll 1
         for (int sub = H::NSUB - 1; sub >= 0; --sub) {
             constexpr int PT = 4 / H::NC;                      // dB, dC values left per step
@@ -1305,67 +1333,76 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                 }
                 const float* Br = Bs + sq * H::RQ + sub * ST * H::RB + 4 * j;
                 const float* Cr = Cs + sq * H::RQ + sub * ST * H::RB + 4 * j;
-                uint64_t a[KL][ST][2], h[KL][ST][2];
-                {
-                    uint64_t du2[KL][ST];
-#pragma unroll
-                    for (int kl = 0; kl < KL; ++kl)
-                        decays<HEADS, ST>(A2[kl], st + so[kl], in.as + so[kl], starts >> (sub * ST) & ((1u << ST) - 1), a[kl], du2[kl]);
-#pragma unroll
-                    for (int i = 0; i < ST; ++i) {
-                        uint64_t bv[2];
-                        ldpair(Br + i * H::RB, bv);
+                const uint32_t cuts = starts_in<ST>(starts, sub);
+                float y[8], s1[8], s2[8];
+                auto steps = [&](auto cutting) {
+                    constexpr bool CUT = decltype(cutting)::value;
+                    uint64_t a[KL][ST][2], h[KL][ST][2];
+                    {
+                        uint64_t du2[KL][ST];
 #pragma unroll
                         for (int kl = 0; kl < KL; ++kl)
+                            decays<HEADS, ST>(A2[kl], st + so[kl], in.as + so[kl], a[kl], du2[kl]);
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                h[kl][i][k] = fma2(a[kl][i][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k],
-                                                   mul2(du2[kl][i], bv[k]));
-                    }
-                }
-                float y[8], s1[8], s2[8];
+                        for (int i = 0; i < ST; ++i) {
+                            uint64_t bv[2];
+                            ldpair(Br + i * H::RB, bv);
 #pragma unroll
-                for (int i = ST - 1; i >= 0; --i) {
-                    uint64_t bv[2], cv[2], tb2[2], tc2[2];
-                    ldpair(Br + i * H::RB, bv);
-                    ldpair(Cr + i * H::RB, cv);
+                            for (int kl = 0; kl < KL; ++kl)
 #pragma unroll
-                    for (int kl = 0; kl < KL; ++kl) {
-                        const float2 s = st[so[kl] + i];
-                        const float g = gs[so[kl] + i];
-                        const uint64_t d2 = pk2(s.x, s.x), du2 = pk2(s.y, s.y), g2 = pk2(g, g);
-                        uint64_t lam[2], q[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            lam[k] = fma2(g2, cv[k], m[kl][k]);
-                            m[kl][k] = mul2(a[kl][i][k], lam[k]);
-                            q[k] = mul2(m[kl][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k]);
-                            dA[kl][k] = fma2(q[k], d2, dA[kl][k]);
-                            tb2[k] = kl ? fma2(lam[k], du2, tb2[k]) : mul2(lam[k], du2);
-                            tc2[k] = kl ? fma2(g2, h[kl][i][k], tc2[k]) : mul2(g2, h[kl][i][k]);
-                        }
-                        const int v = kl * ST + i;
-                        const float2 fy = upk2(fma2(cv[1], h[kl][i][1], mul2(cv[0], h[kl][i][0])));
-                        const float2 f1 = upk2(fma2(bv[1], lam[1], mul2(bv[0], lam[0])));
-                        y[v] = fy.x + fy.y;
-                        s1[v] = f1.x + f1.y;
-                        if constexpr (HEADS) {
-                            const float2 f2 = upk2(add2(q[0], q[1]));
-                            s2[v] = f2.x + f2.y;                // times A: see finish()
-                        } else {
-                            const float2 f2 = upk2(fma2(q[1], A2[kl][1], mul2(q[0], A2[kl][0])));
-                            s2[v] = f2.x + f2.y;
+                                for (int k = 0; k < 2; ++k) {
+                                    uint64_t before = i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k];
+                                    if (CUT && (cuts >> i & 1)) before = 0;
+                                    h[kl][i][k] = fma2(a[kl][i][k], before, mul2(du2[kl][i], bv[k]));
+                                }
                         }
                     }
-                    float vb[PT], vc[PT];
-                    reduce_slots<S>(tb2, vb);
-                    reduce_slots<S>(tc2, vc);
 #pragma unroll
-                    for (int k = 0; k < PT; ++k) {
-                        rB[i * PT + k] = KC > 1 ? rB[i * PT + k] + vb[k] : vb[k];
-                        rC[i * PT + k] = KC > 1 ? rC[i * PT + k] + vc[k] : vc[k];
+                    for (int i = ST - 1; i >= 0; --i) {
+                        uint64_t bv[2], cv[2], tb2[2], tc2[2];
+                        ldpair(Br + i * H::RB, bv);
+                        ldpair(Cr + i * H::RB, cv);
+#pragma unroll
+                        for (int kl = 0; kl < KL; ++kl) {
+                            const float2 s = st[so[kl] + i];
+                            const float g = gs[so[kl] + i];
+                            const uint64_t d2 = pk2(s.x, s.x), du2 = pk2(s.y, s.y), g2 = pk2(g, g);
+                            uint64_t lam[2], q[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                lam[k] = fma2(g2, cv[k], m[kl][k]);
+                                m[kl][k] = mul2(a[kl][i][k], lam[k]);
+                                q[k] = mul2(m[kl][k], i ? h[kl][i ? i - 1 : 0][k] : h0[kl][k]);
+                                if (CUT && (cuts >> i & 1)) m[kl][k] = q[k] = 0;
+                                dA[kl][k] = fma2(q[k], d2, dA[kl][k]);
+                                tb2[k] = kl ? fma2(lam[k], du2, tb2[k]) : mul2(lam[k], du2);
+                                tc2[k] = kl ? fma2(g2, h[kl][i][k], tc2[k]) : mul2(g2, h[kl][i][k]);
+                            }
+                            const int v = kl * ST + i;
+                            const float2 fy = upk2(fma2(cv[1], h[kl][i][1], mul2(cv[0], h[kl][i][0])));
+                            const float2 f1 = upk2(fma2(bv[1], lam[1], mul2(bv[0], lam[0])));
+                            y[v] = fy.x + fy.y;
+                            s1[v] = f1.x + f1.y;
+                            if constexpr (HEADS) {
+                                const float2 f2 = upk2(add2(q[0], q[1]));
+                                s2[v] = f2.x + f2.y;                // times A: see finish()
+                            } else {
+                                const float2 f2 = upk2(fma2(q[1], A2[kl][1], mul2(q[0], A2[kl][0])));
+                                s2[v] = f2.x + f2.y;
+                            }
+                        }
+                        float vb[PT], vc[PT];
+                        reduce_slots<S>(tb2, vb);
+                        reduce_slots<S>(tc2, vc);
+#pragma unroll
+                        for (int k = 0; k < PT; ++k) {
+                            rB[i * PT + k] = KC > 1 ? rB[i * PT + k] + vb[k] : vb[k];
+                            rC[i * PT + k] = KC > 1 ? rC[i * PT + k] + vc[k] : vc[k];
+                        }
                     }
-                }
+                };
+                if (!HEADS && cuts) steps(std::bool_constant<!HEADS>{});
+                else steps(std::false_type{});
                 using Sums = StateSums<S>;
                 Sums::sum(y, lane);
                 Sums::sum(s1, lane);

@@ -222,6 +222,24 @@ def test_rows_of_more_steps_than_a_grid_axis_holds_chunks():
         assert np.all(np.abs(host(getattr(g, k)) - want) <= 1e-2 * np.sqrt(L)), k
 
 
+@pytest.mark.parametrize("cl", [False, True])
+@pytest.mark.parametrize("segments", [1, 3, 7])
+@pytest.mark.parametrize("N,conv", [(1, 0), (5, 4), (16, 4), (32, 0), (64, 4), (128, 0)])
+def test_a_packed_sequence_that_is_not_finite_leaves_the_others(N, conv, segments, cl):
+    """NaN in one sequence's inputs, an infinity in another's incoming gradient: the other
+    sequences' gradients keep their bits."""
+    D, L, starts = 20, 203, [0, 37, 40, 88, 89, 150, 203]
+    c = case(25, "f32", 1, D, L, N, conv=conv)
+    want = call(c, "f32", cl, starts=starts, num_segments=segments)
+    c["u"][0, :, 60], c["delta"][0, ::3, 41], c["dout"][0, :, 140] = np.nan, np.nan, np.inf
+    got = call(c, "f32", cl, starts=starts, num_segments=segments)
+    keep = np.r_[0:40, 88:89, 150:203]
+    for k in LAST:
+        a, o = host(getattr(got, k), cl), host(getattr(want, k), cl)
+        assert np.all(np.isfinite(o)) and np.array_equal(a[..., keep], o[..., keep]), k
+    assert np.isnan(host(got.dC, cl)[..., 60:88]).all()     # the bad one shows it
+
+
 def test_misaligned_rows():
     """Rows whose length and base are not multiples of 16 bytes take the scalar loads."""
     c = case(11, "bf16", 2, 33, 61, 16, conv=4)

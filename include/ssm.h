@@ -369,8 +369,9 @@ typedef struct {
 } ssm_scan_bwd_args_t;
 
 /* Bytes of device workspace the call with these arguments needs. Pointers are only
- * compared with NULL. The larger part holds the states before every 8th step: about
- * batch * dim * seqlen * dstate / 2 bytes. */
+ * compared with NULL. The larger part holds the states before every 4th step (every 8th up
+ * to dstate 8), dstate rounded up to a power of two from 4 on: about batch * dim * seqlen *
+ * dstate bytes (half of it up to 8). */
 SSM_API ssm_status_t ssm_selective_scan_bwd_workspace_size(const ssm_scan_bwd_args_t* args,
                                                            size_t* bytes);
 

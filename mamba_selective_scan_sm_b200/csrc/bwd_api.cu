@@ -88,7 +88,7 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     // the GPU): so a grid that fills three quarters of the SMs' CTA slots is left alone. A
     // smaller one is split so that the waves of CTAs, each as long as a segment's tiles, and the
     // chain over the segments take the least time together: some 7.5 us a tile and 0.3 us a
-    // segment (measured: B8 D1536 L2048 1.00 ms in one sweep, 1.2 in 6 segments; B4 D1536 L2048
+    // segment (measured: B8 D1536 L2048 0.98 ms in one sweep, 1.2 in 6 segments; B4 D1536 L2048
     // 0.88 in one, 0.71 in 6; B1 D5120 L16384 6.0 in one, 3.35 in 9; d_state 128 with A per
     // head, B2 D1536 L2048, 2.48 in one, 1.66 in 3).
     int64_t nseg = a->num_segments;

@@ -11,8 +11,8 @@
 // and d dt = ddelta sigmoid(dt + bias) under the softplus.
 //
 // The recurrence cannot be run backwards from its last state (dividing by a small a_t loses
-// everything), so a forward pass first leaves the state before every T-th step (4, or 8 below
-// d_state 16) in global memory (MODE kCheckpoint), and the backward sweep redoes T steps at a
+// everything), so a forward pass first leaves the state before every T-th step (4, or 8 up to
+// d_state 8) in global memory (MODE kCheckpoint), and the backward sweep redoes T steps at a
 // time from there with a_t and h_t in registers. Two exps per (channel, step, state) in all. A
 // grid too small for the GPU splits the sequence into segments: a first pass (MODE kSummary)
 // reduces each to its decay product, its end state from zero and its adjoint carry from zero,
@@ -80,7 +80,7 @@ template <int S> struct BwdShape {
         return kSt + (heads ? kDecay : 0) + (adj ? kG + kU + 2 * kBC : kBC);
     }
     static constexpr int RP = 2 * NS + 8;                      // row of dB, dC of a step
-    static constexpr int PS = S >= 16 || S == 4 ? T : TT;                // steps of dB, dC summed at a time
+    static constexpr int PS = S >= 16 || S == 4 ? T : TT; // steps of dB, dC summed at a time
     static constexpr int kPart = W * PS * RP;
     static constexpr int kPrm = 8 * G;
     static constexpr int kMask = 4;                            // sequence starts of the two tiles, as bits

@@ -240,6 +240,30 @@ def test_a_packed_sequence_that_is_not_finite_leaves_the_others(N, conv, segment
     assert np.isnan(host(got.dC, cl)[..., 60:88]).all()     # the bad one shows it
 
 
+@pytest.mark.parametrize("cl", [False, True])
+def test_activations_past_32_bit_offsets(cl):
+    """2080 channels of 2^20 steps: the last 32 channels' gradients are those of a call on
+    these alone."""
+    m = ssm()
+    D, L, N, last = 2080, 1 << 20, 1, 32
+    r = torch.Generator(device="cuda").manual_seed(9)
+    act = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=r)  # noqa: E731
+    shape, bc = ((1, L, D), (1, L, N)) if cl else ((1, D, L), (1, N, L))
+    u, delta, dout, B, C = act(*shape), act(*shape), act(*shape), act(*bc), act(*bc)
+    A, w = -torch.rand(D, N, device="cuda", generator=r) - 0.5, torch.randn(D, 4, device="cuda", generator=r) / 2
+    kw = dict(channel_last=cl, num_segments=16)
+    g = m.ssm_selective_scan_bwd(dout, u, delta, A, B, C, conv_weight=w, **kw)
+    end = lambda t: t[..., D - last:] if cl else t[:, D - last:]  # noqa: E731
+    o = m.ssm_selective_scan_bwd(end(dout), end(u), end(delta), A[D - last:], B, C, conv_weight=w[D - last:], **kw)
+    assert torch.equal(end(g.du), o.du) and torch.equal(end(g.ddelta), o.ddelta)
+    assert torch.equal(g.dA[D - last:], o.dA) and torch.equal(g.dconv_weight[D - last:], o.dconv_weight)
+    del g, o
+    packed = m.ssm_checkpoint_pack(u, channel_last=cl)
+    back = end(m.ssm_checkpoint_unpack(packed, channel_last=cl))
+    small = m.ssm_checkpoint_pack(end(u), channel_last=cl)
+    assert torch.equal(back, m.ssm_checkpoint_unpack(small, channel_last=cl))
+
+
 def test_misaligned_rows():
     """Rows whose length and base are not multiples of 16 bytes take the scalar loads."""
     c = case(11, "bf16", 2, 33, 61, 16, conv=4)

@@ -473,9 +473,10 @@ typedef struct {
 
 /* The decode step of ssm_selective_state_update_ex on a cache: reads the row's state from
  * its slot, takes one step in fp32, gives out from the new state before it is rounded, and
- * writes the state back in 8 bits (a quotient within 1e-4 of a border between two codes may
- * take either: the new state's own fp32 rounding is of that size). conv_state is held per
- * slot too. Errors as there; SSM_ERR_BAD_SHAPE also for num_slots < batch without slots,
+ * writes the state back in 8 bits. What is rounded is the new state as fp32 holds it; a quotient
+ * within 1e-5 of a border between two codes may take either, and with rand a quotient plus offset
+ * within 1e-6 of a whole number (the offset's 24th bit is left out). conv_state is held per slot
+ * too. Errors as there; SSM_ERR_BAD_SHAPE also for num_slots < batch without slots,
  * batch * dim from 2^31 and num_slots * dim from 2^32 on. */
 SSM_API ssm_status_t ssm_selective_state_update_cached(const ssm_cached_update_args_t* args,
                                                        ssm_stream_t stream);

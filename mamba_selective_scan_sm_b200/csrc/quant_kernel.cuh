@@ -62,10 +62,12 @@ struct Quant {
         }
     }
     // The same for values that are hardly ever next to a border (fp32 states): one test for
-    // all N, pairs at a time. Without EXACT the fp32 quotient decides borders too: for values
-    // that carry roundings of their own (a state just computed).
+    // all N, pairs at a time. Without EXACT (a state just computed, which carries roundings of
+    // its own) the reciprocal takes a step of Newton's, and the fp32 quotient, off by less than
+    // 1e-5 (127 times two roundings of 2^-24 or so), decides borders too.
     template <bool EXACT, int N> __device__ __forceinline__ void nearest_rare(const float (&x)[N], uint32_t (&q)[N]) const {
-        const uint64_t inv2 = pk2(inv, inv), magic2 = pk2(kMagic, kMagic), minus = pk2(-1.f, -1.f);
+        const float by = EXACT ? inv : fmaf(inv * (1.f / 127.f), lacking(), inv);
+        const uint64_t inv2 = pk2(by, by), magic2 = pk2(kMagic, kMagic), minus = pk2(-1.f, -1.f);
         float worst = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -83,14 +85,18 @@ struct Quant {
     // floor(127 x / top + offset), the offset of value i the top 24 bits of bits + i GOLDEN as
     // a fraction. F = 1 + offset (to 23 bits: the 24th counts next to a border only) comes out
     // of one funnel shift, and x inv + F plus 1.5 2^23 - 1, rounded down, holds the code.
-    // Offsets are random, so quotients next to a border are rare: fp64 there.
+    // EXACT: offsets are random, so quotients next to a border are rare: fp64 there. Otherwise
+    // the quotient gets what the reciprocal lacks, x (inv + lo) + F with the inner sum rounded to
+    // the nearest (at most 2^-24, 2^-23 above 2) and the outer one down, which takes no whole
+    // number from the sum: the code is the floor of the sum to 3e-7 of a step, and right on
+    // average to that. lo is 2^-30 of the reciprocal smaller (1.2e-7 for x = top), more than the
+    // inner rounding, so that top itself never comes out as 128 or -128. (Quotients without lo,
+    // 2^-21 smaller to stay below 128, lost 5e-7 of every state per step.)
     template <bool EXACT, int N>
     __device__ __forceinline__ void dithered(const float (&x)[N], uint32_t bits, uint32_t (&q)[N]) const {
-        // Without the exact test nothing else keeps max / max * 127 + offset below 128: the
-        // quotients are taken 2^-21 smaller, which is more than the reciprocal's and the
-        // product's rounding together.
-        const float by = EXACT ? inv : inv * 0.9999995231628418f;
-        const uint64_t inv2 = pk2(by, by), magic2 = pk2(kMagic - 1.f, kMagic - 1.f), minus = pk2(-1.f, -1.f);
+        const float lo = EXACT ? 0.f : inv * fmaf(lacking(), 1.f / 127.f, -0x1p-30f);
+        const uint64_t inv2 = pk2(inv, inv), lo2 = pk2(lo, lo);
+        const uint64_t magic2 = pk2(kMagic - 1.f, kMagic - 1.f), minus = pk2(-1.f, -1.f);
         const uint64_t half2 = pk2(-0.5f, -0.5f);
         float worst = 0.f;
 #pragma unroll
@@ -98,8 +104,10 @@ struct Quant {
             const uint32_t b0 = bits + (uint32_t)i * 0x9E3779B9u, b1 = bits + (uint32_t)(i + 1) * 0x9E3779B9u;
             const uint64_t f2 = pk2(__uint_as_float(__funnelshift_r(b0, 0x7fu, 9)),
                                     __uint_as_float(__funnelshift_r(b1, 0x7fu, 9)));
-            const uint64_t v = fma2(pk2(x[i], x[i + 1]), inv2, f2);
-            uint64_t t;
+            const uint64_t x2 = pk2(x[i], x[i + 1]);
+            uint64_t v, t;
+            if constexpr (EXACT) v = fma2(x2, inv2, f2);
+            else asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(x2), "l"(inv2), "l"(fma2(x2, lo2, f2)));
             asm("add.rm.f32x2 %0, %1, %2;" : "=l"(t) : "l"(v), "l"(magic2));
             if constexpr (EXACT) {                             // v less its floor, less a half
                 const float2 e = upk2(add2(add2(v, half2), fma2(t, minus, magic2)));
@@ -127,6 +135,8 @@ struct Quant {
     }
 
   private:
+    // 127 - top inv: what the reciprocal lacks (or has too much), times top
+    __device__ __forceinline__ float lacking() const { return inv == 0.f ? 0.f : fmaf(-top, inv, 127.f); }
     // the code of x, whose quotient lies next to m = k + 1/2
     __device__ __forceinline__ int border(float x, float m) const {
         const float sc = top > 1.f ? 0.0009765625f : 1.f;      // keeps 127 top finite
@@ -414,8 +424,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheParams p) {
 // out. ASYNC: codes, scale, conv window and rounding bits come through a ring of asynchronous
 // copies kUpdateStages - 1 rows ahead (rows of 16-byte aligned codes, conv width 4 or none);
 // a thread reads back only what it copied itself. The rows' B and C are staged once as fp32
-// for all channels of the CTA. B256 D5120 N16 bf16 with conv and rounding bits: 28 us, 94 MB
-// (14 us of HBM); the issue slots bind (one row a thread with plain loads: 124 us; with
+// for all channels of the CTA. B256 D5120 N16 bf16 with conv and rounding bits: 30 us, 94 MB
+// (14 us of HBM); the issue slots bind (one row a thread with plain loads: 124 us; without the
+// random rounding's second product, biased: 28 us; with
 // quotients next to a border decided exactly: 43 us).
 constexpr int kUpdateThreads = 128;
 constexpr int kUpdateCtas = 4;                                 // per SM: 128 registers a thread

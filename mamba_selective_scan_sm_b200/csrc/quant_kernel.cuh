@@ -354,13 +354,13 @@ __device__ __forceinline__ int64_t slot_of(const CacheParams& p, int64_t b) {
 // Codes of a row's NP states from first on, and what the row's scale comes from, from LPR
 // lanes of a row.
 template <bool EXACT, int LPR, int NP>
-__device__ __forceinline__ Quant quantise_row(const float (&h)[NP], const uint32_t* rand, int first,
+__device__ __forceinline__ Quant quantise_row(const float (&h)[NP], bool random, uint32_t bits, int first,
                                               uint32_t (&q)[NP]) {
     float top = max_mag(h);
 #pragma unroll
     for (int w = 1; w < LPR; w *= 2) top = max_mag(top, top, __shfl_xor_sync(0xffffffffu, top, w));
     const Quant qz(top);
-    if (rand) qz.dithered<EXACT>(h, *rand + (uint32_t)first * 0x9E3779B9u, q);
+    if (random) qz.dithered<EXACT>(h, bits + (uint32_t)first * 0x9E3779B9u, q);
     else qz.nearest_rare<EXACT>(h, q);
     return qz;
 }
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheParams p) {
     const uint32_t r0 = blockIdx.x * per * kCacheRows + threadIdx.x / LPR;
     float h[kCacheRows][8];
     int64_t at[kCacheRows];                                    // row in the cache, or -1
+    uint32_t bits[kCacheRows];
 #pragma unroll
     for (int k = 0; k < kCacheRows; ++k) {
         const uint32_t row = r0 + k * per;
@@ -385,15 +386,25 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheParams p) {
             const int64_t slot = slot_of(p, b);
             if (slot >= 0) at[k] = slot * dim + (row - b * dim);
         }
-        // whole, aligned rows: no branch comes between the loads
-        if (p.vec) take_run<float, 8>(p.state + (int64_t)min(row, rows - 1) * p.dstate + 8 * j, false, h[k]);
-        else load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, 1, 0, at[k] >= 0 ? n : 0, h[k]);
+    }
+    // a padded row's state and rounding bits are not read: they need not exist
+#pragma unroll
+    for (int k = 0; k < kCacheRows; ++k) {
+        const uint32_t row = r0 + k * per;
+        const bool live = at[k] >= 0;
+        bits[k] = p.rand && live ? p.rand[row] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] = 0.f;
+        if (p.vec) {
+            if (live) take_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, false, h[k]);
+        } else {
+            load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, 1, 0, live ? n : 0, h[k]);
+        }
     }
 #pragma unroll
     for (int k = 0; k < kCacheRows; ++k) {
         uint32_t q[8];
-        const uint32_t* rand = p.rand ? p.rand + (at[k] >= 0 ? r0 + k * per : 0) : nullptr;
-        const Quant qz = quantise_row<true, LPR, 8>(h[k], rand, 8 * j, q);
+        const Quant qz = quantise_row<true, LPR, 8>(h[k], p.rand != nullptr, bits[k], 8 * j, q);
         if (at[k] < 0) continue;
         if (n > 0) store_codes<8>(p.codes + at[k] * p.dstate + 8 * j, n, q);
         if (j == 0) p.scales[at[k]] = qz.scale();
@@ -457,7 +468,8 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
     for (int k = threadIdx.x; k < rows * 2 * NS; k += kUpdateThreads) {
         const int r = k / (2 * NS), which = k / NS % 2, i = k % NS;
         const T* src = static_cast<const T*>(which ? p.Ct : p.Bt);
-        bc[r][which][i] = i < p.dstate ? E::to_f(src[(b0 + r) * p.dstate + i]) : 0.f;
+        const bool read = i < p.dstate && slot_of(p, b0 + r) >= 0;  // nothing of a padded row
+        bc[r][which][i] = read ? E::to_f(src[(b0 + r) * p.dstate + i]) : 0.f;
     }
     if (threadIdx.x < rows) slot_sm[threadIdx.x] = (int)slot_of(p, b0 + threadIdx.x);
     float A2[16], w[4], cb = 0.f, Dv = 0.f, bias = 0.f;
@@ -618,7 +630,7 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
 #pragma unroll
         for (int k = 1; k < LPR; k *= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
         uint32_t q[16];
-        const Quant qz = quantise_row<false, LPR, 16>(h, p.rand ? &v.rand : nullptr, 16 * j, q);
+        const Quant qz = quantise_row<false, LPR, 16>(h, p.rand != nullptr, v.rand, 16 * j, q);
         if (!live) continue;
         if (n > 0) store_codes<16>(codes_at(at), n, q);
         if (j == 0) {

@@ -1,0 +1,75 @@
+"""Sums over very long rows in the scan's gradient, where the terms have one sign and a plain
+fp32 sum would lose them; and steps that leave the states as they are."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def ssm():
+    import mamba_selective_scan_sm_b200 as m
+    return m
+
+
+def closed_form(L, A, d):
+    """The gradients' sums for u = B = dout = 1, C = 1 / N, delta = d at every step, in double
+    precision: h and lambda are geometric sums."""
+    D, N = A.shape
+    t = np.arange(L, dtype=np.float64)
+    dA, dbias = np.zeros((D, N)), np.zeros(D)
+    for c in range(D):
+        inner, through = np.zeros(L), np.zeros(L)
+        for n in range(N):
+            a = np.exp(d * A[c, n])
+            lam = (1 - a ** (L - t)) / (1 - a) / N
+            q = lam * a * d * (1 - a ** t) / (1 - a)             # h_{t-1}: t steps behind it
+            dA[c, n] = d * q.sum()
+            inner += lam
+            through += q * A[c, n]
+        dbias[c] = (inner + through).sum()
+    return dA, dbias
+
+
+@pytest.mark.parametrize("cl", [False, True])
+@pytest.mark.parametrize("N", [1, 5, 16, 32, 128])
+def test_terms_of_one_sign(N, cl):
+    """2^19 and more steps in one segment. A decay of at most e^-0.25 = 0.78 is off by 2^-22
+    relative, h and lambda by 4.5 times that, their product by 2.2e-6; 512 additions of one sign
+    add at most 2^-25 each on average (1.5e-5) before a sum joins the others: 2e-5."""
+    m = ssm()
+    L, D, d = (1 << 19) + 40, 3, 0.5
+    A = -np.linspace(0.5, 4.0, D * N).reshape(D, N).astype(np.float32)
+    want_A, want_bias = closed_form(L, A.astype(np.float64), d)
+    one = lambda *s: torch.ones(s, device="cuda")  # noqa: E731
+    act, bc = ((1, L, D), (1, L, N)) if cl else ((1, D, L), (1, N, L))
+    g = m.ssm_selective_scan_bwd(one(*act), one(*act), d * one(*act), torch.from_numpy(A).cuda(), one(*bc),
+                                 one(*bc) / N, one(D), None, torch.zeros(D, device="cuda"), False,
+                                 channel_last=cl, num_segments=1)
+    for k, o in (("dA", want_A), ("ddelta_bias", want_bias), ("dD", np.full(D, float(L)))):
+        got = getattr(g, k).cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - o) <= 2e-5 * np.abs(o)), (k, got / o - 1)
+
+
+@pytest.mark.parametrize("cl", [False, True])
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("N,heads", [(1, 0), (5, 0), (16, 0), (24, 0), (128, 0), (16, 2), (128, 4)])
+def test_steps_without_time_change_no_bit(N, heads, segments, cl):
+    """delta = 0 at every step (and the steps that fill the last tile): the decay is 1 exactly,
+    so the gradient of the last state is that of the first, and dC is g times that state."""
+    m = ssm()
+    B, D, L = 2, 36, 5003
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    A = -torch.rand(heads, generator=g, device="cuda") - 1 if heads else -r(D, N).abs() - 0.5
+    h0, dhl = r(B, D, N), r(B, D, N)
+    t = lambda v: v.transpose(1, 2).contiguous() if cl else v  # noqa: E731
+    zero = torch.zeros(B, D, L, device="cuda")
+    dout = zero.clone()
+    dout[:, 7, 4000] = 1.0
+    out = m.ssm_selective_scan_bwd(t(dout), t(r(B, D, L)), t(zero), A, t(r(B, N, L)), t(torch.zeros(B, N, L, device="cuda")),
+                                   delta_softplus=False, initial_state=h0, dfinal_state=dhl, channel_last=cl,
+                                   num_segments=segments)
+    assert torch.equal(out.dinitial_state, dhl)
+    dC = t(out.dC)
+    assert torch.equal(dC[:, :, 4000], h0[:, 7])

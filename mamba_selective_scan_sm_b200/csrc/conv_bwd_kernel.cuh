@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const 
     const float bias = p.bias ? p.bias[d] : 0.f;
     float sw[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
     if (t0 < L) {
-        // x[t0 - 3 .. t0 + 10], dpre[t0 .. t0 + 10]
+        // x[t0 - 3 .. t0 + R + 2], dpre[t0 .. t0 + R + 2]
         float x[R + 6], dp[R + 3];
         const bool rev = p.reverse;
         const int pos0 = rev ? L - 1 - t0 : t0;
@@ -125,13 +125,15 @@ __global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const 
                                     : Elem<T>::to_f(static_cast<const T*>(p.dout)[o]);
             }
         }
-        float dx[R + 3];                                       // dx[t0 - 3 .. t0 + 7]
+        float dx[R + 3];                                       // dx[t0 - 3 .. t0 + R - 1]
 #pragma unroll
         for (int i = 0; i < R + 3; ++i) dx[i] = 0.f;
-        auto steps = [&](auto packed) {
+        // cut: only the taps within the conv's width and the sequence (an absent tap is no
+        // product with 0, which a NaN or an infinity would pass)
+        auto steps = [&](auto cut) {
 #pragma unroll
             for (int i = 0; i < R + 3; ++i) {
-                const int sn = decltype(packed)::value && t0 + i < L ? p.since[t0 + i] : 4;
+                const int sn = decltype(cut)::value ? min(p.since && t0 + i < L ? p.since[t0 + i] : 4, p.width - 1) : 4;
                 if (p.silu) {
                     float pre = bias;
 #pragma unroll
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const 
                 if (i < R) sw[4] += dp[i];
             }
         };
-        if (p.since) steps(std::true_type{});
+        if (p.since || p.width < 4) steps(std::true_type{});
         else steps(std::false_type{});
         float out[R];
 #pragma unroll
@@ -263,14 +265,15 @@ __global__ void __launch_bounds__(128) conv_bwd_cl_kernel(const ConvBwdParams p)
             }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) sn[k] = p.since ? p.since[min(tu + k, L - 1)] : 4;
+        for (int k = 0; k < U; ++k)                            // the furthest tap that is not cut
+            sn[k] = min(p.since ? p.since[min(tu + k, L - 1)] : 4, p.width - 1);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int t = tu + k;
             if (t >= te + 3) break;
             if (t < L) scaled(t, x[k]);
             float out[E];
-            auto step = [&](auto within) {                     // all 4 taps lie within the sequence
+            auto step = [&](auto within) {                     // all 4 taps are there, within the sequence
                 constexpr bool all = decltype(within)::value;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {

@@ -668,7 +668,7 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
                        : 0.f;
         };
         if constexpr (CL) {
-            const int sn = p.since ? since[r.tl] : 4;
+            const int sn = min(p.since ? since[r.tl] : 4, p.conv_width - 1);   // the furthest tap
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = fmaf(prm[r.c(i) * 8 + 3], u[i], acc[i]);
 #pragma unroll
@@ -709,15 +709,15 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = prm[r.ch * 8 + k];
             auto tap = [&](int i, int lag) { return i >= lag ? u[i >= lag ? i - lag : 0] : xh[i >= lag ? 0 : 3 + i - lag]; };
-            if (!p.since) {
+            if (!p.since && p.conv_width == 4) {
 #pragma unroll
                 for (int i = 0; i < E; ++i)
 #pragma unroll
                     for (int lag = 0; lag < 4; ++lag) acc[i] = fmaf(w[3 - lag], tap(i, lag), acc[i]);
-            } else {
+            } else {                                           // an absent tap is no product with 0
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    const int sn = since[r.tl + i];
+                    const int sn = min(p.since ? since[r.tl + i] : 4, p.conv_width - 1);
 #pragma unroll
                     for (int lag = 0; lag < 4; ++lag)
                         if (lag <= sn) acc[i] = fmaf(w[3 - lag], tap(i, lag), acc[i]);

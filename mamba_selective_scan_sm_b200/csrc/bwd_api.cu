@@ -16,7 +16,7 @@ struct BwdPlan {
     BwdVariant v;
     int groups, nseg, seg_len, nsub, conv_chunks;
     // byte offsets of the workspace's parts
-    size_t ckpt, parts, pA, pD, sumP, sumS, sumR, since, du32, conv_part, total;
+    size_t ckpt, parts, pA, pA_lo, pD, sumP, sumS, sumR, since, du32, conv_part, total;
 };
 
 ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
@@ -127,6 +127,7 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     take(empty ? 0 : (size_t)Bn * pl->nsub * dns, &pl->ckpt);
     take(empty ? 0 : (size_t)pl->groups * Bn * L * 2 * ns * 4, &pl->parts);
     take(empty ? 0 : rows * dns, &pl->pA);
+    take(empty || per <= pl->v.drain ? 0 : rows * dns, &pl->pA_lo);
     take(empty ? 0 : rows * D * 8, &pl->pD);
     const size_t sum = empty || pl->nseg == 1 ? 0 : rows * dns;
     take(sum, &pl->sumP);
@@ -303,6 +304,7 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     p.nsub = pl.nsub;
     p.parts = f(pl.parts);
     p.pA = f(pl.pA);
+    p.pA_lo = f(pl.pA_lo);
     p.pD = f(pl.pD);
     p.sumP = f(pl.sumP);
     p.sumS = f(pl.sumS);

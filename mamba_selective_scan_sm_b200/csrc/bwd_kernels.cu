@@ -72,28 +72,29 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_a_kernel(const BwdReduceP
     if (idx < na) {
         const int d = (int)(idx / p.ns), n = (int)(idx % p.ns) ^ (d >> p.order_shift & p.order_mask);
         if (n >= p.dstate) return;
-        float v = 0.f;
+        LongSum v;
 #pragma unroll 8
-        for (int r = 0; r < p.nrows; ++r) v += p.pA[r * na + idx];
-        p.dA[(int64_t)d * p.dstate + n] = v;
+        for (int r = 0; r < p.nrows; ++r) v.add(p.pA[r * na + idx]);
+        p.dA[(int64_t)d * p.dstate + n] = v.get();
     } else if (idx < na + 2 * (int64_t)p.dim) {
         const int64_t k = idx - na;
         float* o = k % 2 ? p.dbias : p.dD;
         if (!o) return;
-        float v = 0.f;
+        LongSum v;
 #pragma unroll 8
-        for (int r = 0; r < p.nrows; ++r) v += p.pD[(int64_t)r * p.dim * 2 + k];
-        o[k / 2] = v;
+        for (int r = 0; r < p.nrows; ++r) v.add(p.pD[(int64_t)r * p.dim * 2 + k]);
+        o[k / 2] = v.get();
     }
 }
 
 __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdReduceParams p) {
     const int h = blockIdx.x;
-    float v = 0.f;
+    LongSum sum;
     for (int r = 0; r < p.nrows; ++r) {                        // (nrows, dim): summed over the states
         const float* src = p.pA + (int64_t)r * p.dim + (int64_t)h * p.head_dim;
-        for (int k = threadIdx.x; k < p.head_dim; k += blockDim.x) v += src[k];
+        for (int k = threadIdx.x; k < p.head_dim; k += blockDim.x) sum.add(src[k]);
     }
+    float v = sum.get();
     __shared__ float red[256 / 32];
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdRed
 
 template <int S> static BwdVariant variant_of() {
     using H = BwdShape<S>;
-    return {H::NS, H::G, H::TT, H::T, H::CTAS, H::KL - 1, H::NC - 1};
+    return {H::NS, H::G, H::TT, H::T, H::DRAIN, H::CTAS, H::KL - 1, H::NC - 1};
 }
 BwdVariant scan_bwd_variant(int lanes) {
     return lanes == 1   ? variant_of<1>()

@@ -11,6 +11,7 @@ namespace ssm {
 struct BwdVariant {
     int ns, channels, tile;
     int steps;                    // between two checkpoints of the state
+    int drain;                    // tiles between two additions to the sums over a segment
     int ctas;                     // of the backward sweep per SM
     int order_shift, order_mask;  // scratch states of channel d stand at n ^ (d >> shift & mask)
 };

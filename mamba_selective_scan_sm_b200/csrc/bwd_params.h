@@ -45,6 +45,7 @@ struct BwdParams {
     int nsub;                     // checkpoints per row, of whole tiles
     float* parts;                 // (groups, batch, seqlen, 2, NS): dB, dC of a channel group
     float* pA;                    // (nseg * batch, dim, NS); with A per head (nseg * batch, dim)
+    float* pA_lo;                 // as pA, for segments longer than a drain: what its sums round off
     float* pD;                    // (nseg * batch, dim, 2): dD, d delta_bias
     float *sumP, *sumS, *sumR;    // (nseg, batch, dim, NS) segment summaries, then carries
     int nseg, seg_len;

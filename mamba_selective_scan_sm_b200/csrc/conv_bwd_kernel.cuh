@@ -333,11 +333,12 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(const ConvReduceParams
     __shared__ float red[8][32];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t idx = (int64_t)blockIdx.x * 32 + lane;
-    float v = 0.f;
+    LongSum sum;
     if (idx < (int64_t)p.dim * 5) {
 #pragma unroll 8
-        for (int64_t r = warp; r < p.rows; r += 8) v += p.part[r * p.dim * 5 + idx];
+        for (int64_t r = warp; r < p.rows; r += 8) sum.add(p.part[r * p.dim * 5 + idx]);
     }
+    float v = sum.get();
     red[warp][lane] = v;
     __syncthreads();
     if (warp != 0 || idx >= (int64_t)p.dim * 5) return;

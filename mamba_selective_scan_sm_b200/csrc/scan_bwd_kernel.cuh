@@ -49,6 +49,22 @@ namespace ssm {
 constexpr int kCheckpoint = 0, kSummary = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// A sum of many terms: the fp32 sum and, beside it, the sum of what its additions rounded off
+// (exact, by the two-sum). A plain fp32 sum of terms of one sign loses 2^-25 of itself per
+// addition: over 2^19 steps 0.5 %.
+struct LongSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float t = hi + x, b = t - hi;
+        lo += (hi - (t - b)) + (x - b);
+        hi = t;
+    }
+    __device__ __forceinline__ float get() const {             // (an infinity stays one)
+        return fabsf(lo) < INFINITY ? hi + lo : hi;
+    }
+};
+constexpr int kDrainSteps = 512;  // steps between two additions to the long sums
+
 // Static shape of the kernels for S lanes per channel.
 template <int S> struct BwdShape {
     static constexpr int NS = 4 * S;                           // states, padded
@@ -64,6 +80,7 @@ template <int S> struct BwdShape {
     static constexpr int G = W * CW * KL * KC;                 // channels per CTA
     static constexpr int TT = S == 4 ? 16 : 8;                 // steps per tile
     static constexpr int NSUB = TT / T;
+    static constexpr int DRAIN = kDrainSteps / TT;             // tiles
     static constexpr int EPT = G * TT / NH;                    // elements per helper and tensor
     static constexpr int RB = NS;                              // row of B / C in floats
     // shared memory, in floats
@@ -1113,10 +1130,27 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
         // tile n - 1, then tile n + 1 into the staged tile that n - 1 leaves.
         const int hid = tid - 32 * H::W;
         const BwdRun<S, CL> run(hid);
-        float dD = 0.f, dBias = 0.f;
+        LongSum dD, dBias;                                     // rows: of the run's channel; CL: of channel hid
         if constexpr (CL) {
             for (int k = hid; k < H::kSum; k += H::NH) sums[k] = 0.f;
         }
+        // channel-last: the sums of a tile's places, one thread a channel
+        auto drain = [&] {
+            static_assert(H::G <= H::NH, "a thread per channel");
+            named_bar_sync(1, H::NH);
+            if (hid < H::G) {
+                float v0 = 0.f, v1 = 0.f;
+                for (int t = 0; t < TT; ++t) {
+                    float *a = sums + hid * TT + t, *b = a + H::G * TT;
+                    v0 += *a;
+                    v1 += *b;
+                    *a = *b = 0.f;
+                }
+                dD.add(v0);
+                dBias.add(v1);
+            }
+            named_bar_sync(1, H::NH);
+        };
         auto start = [&](int n) { return tb + (ntiles - 1 - n) * TT; };
         auto fetch = [&](int n) {
             fetch_tile<T, S, CL, Q8, true>(p, table, hid, b, d0, start(n), raw + n % 3 * kRaw);
@@ -1167,8 +1201,10 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                         tileBias += ddt[i];                    // the long sum
                     }
                 }
-                dD += tileD;
-                dBias += tileBias;
+                if constexpr (!CL) {
+                    dD.add(tileD);
+                    dBias.add(tileBias);
+                }
                 if constexpr (CL) {
                     auto at = [&](const Str& s) { return (int64_t)b * s.b + d + (int64_t)pos * s.p; };
                     if (p.du32) put_run<float, E>(p.du32 + at(p.sdu), false, p.vec_out, hi, du);
@@ -1193,6 +1229,7 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
         for (int n = -1; n < ntiles; ++n) {
             cp_async_wait();
             if (n > 0) finish(n - 1);
+            if (CL && n > 0 && n % H::DRAIN == 0) drain();
             named_bar_sync(1, H::NH);                          // tile n + 1 is here, n - 1 finished
             if (n + 2 < ntiles) fetch(n + 2);
             if (n + 1 < ntiles) stage(n + 1);
@@ -1202,28 +1239,23 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
         if constexpr (!CL) {
             // the threads of a channel are neighbours within a warp (TT / EPT of them)
             constexpr int PER = TT / E;
+            float v0 = dD.get(), v1 = dBias.get();
 #pragma unroll
             for (int w = 1; w < PER; w *= 2) {
-                dD += __shfl_xor_sync(0xffffffffu, dD, w);
-                dBias += __shfl_xor_sync(0xffffffffu, dBias, w);
+                v0 += __shfl_xor_sync(0xffffffffu, v0, w);
+                v1 += __shfl_xor_sync(0xffffffffu, v1, w);
             }
             if (hid % PER == 0 && d0 + run.ch < p.dim) {
                 float* o = p.pD + (row * p.dim + d0 + run.ch) * 2;
-                o[0] = dD;
-                o[1] = dBias;
-            }
-        } else {
-            named_bar_sync(1, H::NH);
-            for (int c = hid; c < H::G; c += H::NH) {
-                if (d0 + c >= p.dim) break;
-                float v0 = 0.f, v1 = 0.f;
-                for (int t = 0; t < TT; ++t) {
-                    v0 += sums[c * TT + t];
-                    v1 += sums[H::G * TT + c * TT + t];
-                }
-                float* o = p.pD + (row * p.dim + d0 + c) * 2;
                 o[0] = v0;
                 o[1] = v1;
+            }
+        } else {
+            drain();
+            if (hid < H::G && d0 + hid < p.dim) {
+                float* o = p.pD + (row * p.dim + d0 + hid) * 2;
+                o[0] = dD.get();
+                o[1] = dBias.get();
             }
         }
         return;
@@ -1264,6 +1296,60 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
     for (int kl = 0; kl < KL; ++kl) hn[kl][0] = hn[kl][1] = 0;
     load_ckpt(0);
     int left = ntiles * H::NSUB;                               // sub-tiles to come
+    // dA of the steps since the last call: added to the long sums in scratch memory (every DRAIN
+    // tiles), or (last) the whole sum left there. A thread comes back to the places it wrote.
+    auto drain = [&](bool first, bool last) {
+        auto put = [&](int64_t o, float v) {
+            LongSum s;
+            if (!first) {
+                s.hi = p.pA[o];
+                s.lo = p.pA_lo[o];
+            }
+            s.add(v);
+            p.pA[o] = last ? s.get() : s.hi;
+            if (!last) p.pA_lo[o] = s.lo;
+        };
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+#pragma unroll
+            for (int kl = 0; kl < KL; ++kl) {
+                const int d = d0 + H::channel(warp, kc, cl, j, kl);
+                if constexpr (!REGS) ldpair(place(kc, kl) + 4, dA[kl]);
+                if (!HEADS && d < p.dim) {
+                    const int64_t o = ns_off<S>(p, row, d, j);
+                    if (first && last) {
+                        stpair(p.pA + o, dA[kl]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 f = upk2(dA[kl][k]);
+                            put(o + 2 * k, f.x);
+                            put(o + 2 * k + 1, f.y);
+                        }
+                    }
+                }
+            }
+            if constexpr (HEADS) {                             // (rows, dim): summed over the states
+                constexpr bool kTrade = StateSums<S>::kTrade;
+                float v[KL];
+#pragma unroll
+                for (int kl = 0; kl < KL; ++kl) {
+                    const float2 f = upk2(add2(dA[kl][0], dA[kl][1]));
+                    v[kl] = f.x + f.y;
+                }
+                if constexpr (kTrade) v[0] += __shfl_xor_sync(0xffffffffu, v[KL - 1], 1);
+#pragma unroll
+                for (int w = kTrade ? 2 : 1; w < S; w *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
+                const int d = d0 + H::channel(warp, kc, cl, j, 0);
+                if (j < (kTrade ? 2 : 1) && d < p.dim) put(row * p.dim + d, v[0]);
+            }
+#pragma unroll
+            for (int kl = 0; kl < KL; ++kl) {
+                dA[kl][0] = dA[kl][1] = 0;
+                if constexpr (!REGS) stpair(place(kc, kl) + 4, dA[kl]);
+            }
+        }
+    };
     // the CTA's dB and dC of the PS steps from t on: the sum over its warps
     auto flush = [&](int t) {
         constexpr int ROW = 2 * H::NS, PS = H::PS;
@@ -1450,21 +1536,19 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
             if constexpr (H::PS == ST) flush(t0 + sub * ST);   // the next sub-tile takes its place
         }
         if constexpr (H::PS == TT) flush(t0);
+        if ((n + 1) % H::DRAIN == 0 && n + 1 < ntiles) drain(n + 1 == H::DRAIN, false);
         __syncthreads();                                       // tile n is done, n + 1 staged
     }
     // what the sweep summed over its steps
+    drain(ntiles <= H::DRAIN, true);
+    if (seg == 0 && p.dh0) {
 #pragma unroll
-    for (int kc = 0; kc < KC; ++kc) {
+        for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
-        for (int kl = 0; kl < KL; ++kl) {
-            const int d = d0 + H::channel(warp, kc, cl, j, kl);
-            if constexpr (!REGS) {
-                ldpair(place(kc, kl), m[kl]);
-                ldpair(place(kc, kl) + 4, dA[kl]);
-            }
-            if (d >= p.dim) continue;
-            if constexpr (!HEADS) stpair(p.pA + ns_off<S>(p, row, d, j), dA[kl]);
-            if (seg == 0 && p.dh0) {
+            for (int kl = 0; kl < KL; ++kl) {
+                const int d = d0 + H::channel(warp, kc, cl, j, kl);
+                if constexpr (!REGS) ldpair(place(kc, kl), m[kl]);
+                if (d >= p.dim) continue;
                 const float2 lo = upk2(m[kl][0]), hi = upk2(m[kl][1]);
                 const float f[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
@@ -1473,21 +1557,6 @@ __global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_k
                     if (n < p.dstate) p.dh0[((int64_t)b * p.dim + d) * p.dstate + n] = f[k];
                 }
             }
-        }
-        if constexpr (HEADS) {                                 // (rows, dim): summed over the states
-            constexpr bool kTrade = StateSums<S>::kTrade;
-            float v[KL];
-#pragma unroll
-            for (int kl = 0; kl < KL; ++kl) {
-                const float2 f = upk2(add2(dA[kl][0], dA[kl][1]));
-                v[kl] = f.x + f.y;
-            }
-            if constexpr (kTrade) v[0] += __shfl_xor_sync(0xffffffffu, v[KL - 1], 1);
-#pragma unroll
-            for (int w = kTrade ? 2 : 1; w < S; w *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], w);
-            const int d = d0 + H::channel(warp, kc, cl, j, 0);
-            if (j < (kTrade ? 2 : 1) && d < p.dim) p.pA[row * p.dim + d] = v[0];
-        }
     }
 }
 

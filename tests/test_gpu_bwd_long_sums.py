@@ -15,20 +15,12 @@ def ssm():
 def closed_form(L, A, d):
     """The gradients' sums for u = B = dout = 1, C = 1 / N, delta = d at every step, in double
     precision: h and lambda are geometric sums."""
-    D, N = A.shape
-    t = np.arange(L, dtype=np.float64)
-    dA, dbias = np.zeros((D, N)), np.zeros(D)
-    for c in range(D):
-        inner, through = np.zeros(L), np.zeros(L)
-        for n in range(N):
-            a = np.exp(d * A[c, n])
-            lam = (1 - a ** (L - t)) / (1 - a) / N
-            q = lam * a * d * (1 - a ** t) / (1 - a)             # h_{t-1}: t steps behind it
-            dA[c, n] = d * q.sum()
-            inner += lam
-            through += q * A[c, n]
-        dbias[c] = (inner + through).sum()
-    return dA, dbias
+    a = np.exp(d * A)                                        # lambda_t = (1 - a^(L-t)) / (1 - a) / N
+    aL, n = a ** L, A.shape[1]                               # h_(t-1) = d (1 - a^t) / (1 - a)
+    up, down = (1 - aL) / (1 - a), a * (1 - aL) / (1 - a)    # sums of a^t and of a^(L-t)
+    lam = (L - down) / (1 - a) / n
+    q = a * d * (L - down - up + L * aL) / (1 - a) ** 2 / n
+    return d * q, (lam + q * A).sum(1)
 
 
 @pytest.mark.parametrize("cl", [False, True])

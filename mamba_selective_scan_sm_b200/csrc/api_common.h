@@ -56,29 +56,31 @@ inline ssm_status_t check_aligned(const Arg (&args)[N]) {
     return SSM_OK;
 }
 
+// Whether two arguments share an element. Two with the same step may interleave (columns of
+// one tensor).
+inline bool share(const Arg& a, const Arg& b) {
+    if (!ranges_overlap(a.p, a.bytes, b.p, b.bytes)) return false;
+    const auto pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    const Arg &x = pa >= pb ? a : b, &y = pa >= pb ? b : a;    // x's first row among y's rows
+    if (x.step == 0 || x.step != y.step) return true;
+    const size_t d = (pa >= pb ? pa - pb : pb - pa) % x.step;
+    return d < y.row || x.step - d < x.row;
+}
+
 template <int NO, int NI>
 inline ssm_status_t check_alias(const Arg (&outs)[NO], const Arg (&ins)[NI]) {
     for (const Arg& o : outs)
         for (const Arg& i : ins)
-            if (ranges_overlap(o.p, o.bytes, i.p, i.bytes))
-                return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", o.name, i.name);
+            if (share(o, i)) return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", o.name, i.name);
     return SSM_OK;
 }
 
-// Two outputs may interleave (columns of one tensor) but not share an element.
 template <int N>
 inline ssm_status_t check_distinct(const Arg (&outs)[N]) {
     for (int i = 0; i < N; ++i)
-        for (int k = 0; k < i; ++k) {
-            const bool later = reinterpret_cast<uintptr_t>(outs[i].p) >= reinterpret_cast<uintptr_t>(outs[k].p);
-            const Arg &x = later ? outs[i] : outs[k], &y = later ? outs[k] : outs[i];
-            if (!ranges_overlap(x.p, x.bytes, y.p, y.bytes)) continue;
-            if (x.step != 0 && x.step == y.step) {             // x's first row among y's rows
-                const size_t d = (reinterpret_cast<uintptr_t>(x.p) - reinterpret_cast<uintptr_t>(y.p)) % x.step;
-                if (d >= y.row && x.step - d >= x.row) continue;
-            }
-            return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
-        }
+        for (int k = 0; k < i; ++k)
+            if (share(outs[i], outs[k]))
+                return api_fail(SSM_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
     return SSM_OK;
 }
 

@@ -175,12 +175,16 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
     const size_t hist_bytes = a->conv_weight ? (size_t)Bn * D * (a->conv_width - 1) * es : 0;
     const size_t a_bytes = (a->a_heads > 0 ? (size_t)a->a_heads : (size_t)D * N) * 4;
     const size_t w_bytes = a->conv_weight ? (size_t)D * a->conv_width * 4 : 0;
+    // a view in rows, dense ones without a step
+    auto view = [&](const void* q, int64_t st, int64_t width, size_t size, const char* name) {
+        return cl ? Arg{q, size, span(st, width, size), name, (size_t)width * size, (size_t)(st ? st : width) * size}
+                  : Arg{q, size, span(st, width, size), name};
+    };
     const Arg ins[] = {
-        {a->u, ein, span(a->stride_u, D, ein), "u"},
-        {a->delta, ein, span(a->stride_delta, D, ein), "delta"},
-        {a->z, ein, span(a->stride_z, D, ein), "z"},
-        {a->B, es, span(a->stride_B, N, es), "B"}, {a->C, es, span(a->stride_C, N, es), "C"},
-        {a->dout, es, span(a->stride_dout, D, es), "dout"}, {a->A, 4, a_bytes, "A"},
+        view(a->u, a->stride_u, D, ein, "u"), view(a->delta, a->stride_delta, D, ein, "delta"),
+        view(a->z, a->stride_z, D, ein, "z"), view(a->B, a->stride_B, N, es, "B"),
+        view(a->C, a->stride_C, N, es, "C"), view(a->dout, a->stride_dout, D, es, "dout"),
+        {a->A, 4, a_bytes, "A"},
         {a->D, 4, (size_t)D * 4, "D"}, {a->delta_bias, 4, (size_t)D * 4, "delta_bias"},
         {a->conv_weight, 4, w_bytes, "conv_weight"}, {a->conv_bias, 4, (size_t)D * 4, "conv_bias"},
         {a->initial_state, 4, st_bytes, "initial_state"}, {a->dfinal_state, 4, st_bytes, "dfinal_state"},
@@ -188,14 +192,10 @@ ssm_status_t ssm_selective_scan_bwd(const ssm_scan_bwd_args_t* a, ssm_stream_t s
         {a->seq_starts, 4, a->seq_starts ? ((size_t)a->num_seqs + 1) * 4 : 0, "seq_starts"},
         {a->u_scale, 4, sc_bytes, "u_scale"}, {a->delta_scale, 4, sc_bytes, "delta_scale"},
         {a->z_scale, 4, sc_bytes, "z_scale"}};
-    auto rows_out = [&](const void* q, int64_t st, int64_t width, const char* name) {
-        return cl ? Arg{q, es, span(st, width, es), name, (size_t)width * es, (size_t)(st ? st : width) * es}
-                  : Arg{q, es, span(st, width, es), name};
-    };
     const Arg outs[] = {
-        rows_out(a->du, a->stride_du, D, "du"), rows_out(a->ddelta, a->stride_ddelta, D, "ddelta"),
-        rows_out(a->dz, a->stride_dz, D, "dz"), rows_out(a->dB, a->stride_dB, N, "dB"),
-        rows_out(a->dC, a->stride_dC, N, "dC"),
+        view(a->du, a->stride_du, D, es, "du"), view(a->ddelta, a->stride_ddelta, D, es, "ddelta"),
+        view(a->dz, a->stride_dz, D, es, "dz"), view(a->dB, a->stride_dB, N, es, "dB"),
+        view(a->dC, a->stride_dC, N, es, "dC"),
         {a->dA, 4, a_bytes, "dA"}, {a->dD, 4, (size_t)D * 4, "dD"},
         {a->ddelta_bias, 4, (size_t)D * 4, "ddelta_bias"},
         {a->dconv_weight, 4, w_bytes, "dconv_weight"}, {a->dconv_bias, 4, (size_t)D * 4, "dconv_bias"},

@@ -19,6 +19,26 @@ struct BwdPlan {
     size_t ckpt, parts, pA, pA_lo, pD, sumP, sumS, sumR, since, du32, conv_part, total;
 };
 
+// Time of `ctas` CTAs on the GPU, in that of one alone on an SM. Up to per_sm share one, and k of
+// them take 1 + share (k - 1) times as long as one alone: they wait for one another's latencies
+// rather than for a pipe.
+double waves(int64_t ctas, int per_sm, double share) {
+    const int64_t full = ctas / (kNumSMs * per_sm), rest = ctas % (kNumSMs * per_sm);
+    const int64_t k = (rest + kNumSMs - 1) / kNumSMs;
+    return full * (1 + share * (per_sm - 1)) + (rest ? 1 + share * (k - 1) : 0);
+}
+
+// Time (us) of a backward pass in n segments of per tiles, one more to fill and drain each: 0.65
+// of a tile's time is the sweep's, 0.35 the checkpoint pass's, which runs with twice the CTAs an
+// SM; segments add the summary pass, as long, and the chain. A tile's time in us, by lanes a
+// channel (d_state 1..4, 8, 16 (tiles of 16 steps), 32, 64, 128), of one CTA an SM.
+double sweep_time(const BwdVariant& v, int lanes, int64_t ctas, int64_t per, int64_t n) {
+    const double tile = lanes == 1 ? 3.3 : lanes == 2 ? 2.5 : lanes == 4 ? 4.4 : lanes == 8 ? 2.7 : lanes == 16 ? 7.5 : 16;
+    return tile * (per + 1) *
+               (0.65 * waves(ctas * n, v.ctas, 0.7) + 0.35 * (n > 1 ? 2 : 1) * waves(ctas * n, 2 * v.ctas, 0.35)) +
+           (n > 1 ? 0.6 * n : 0);
+}
+
 ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     if (!a) return api_fail(SSM_ERR_NULL_ARG, "args is NULL");
     if (bad_dtype(a->dtype))
@@ -80,31 +100,32 @@ ssm_status_t plan_bwd(const ssm_scan_bwd_args_t* a, BwdPlan* pl) {
     const int64_t Bn = a->batch, D = a->dim, L = a->seqlen;
     pl->lanes = 1;
     while (4 * pl->lanes < a->dstate) pl->lanes *= 2;
-    pl->v = scan_bwd_variant(pl->lanes);
+    pl->v = scan_bwd_variant(pl->lanes, size_of(a->dtype), a->a_heads > 0);
     const int64_t tile = pl->v.tile, ntiles = std::max<int64_t>(1, (L + tile - 1) / tile);
     pl->groups = (int)((D + pl->v.channels - 1) / pl->v.channels);
-    // Segments. One sweep per row takes two exps per (channel, step, state), segments a third
-    // and one more pass over the inputs (about 1.3 times the time where one sweep per row fills
-    // the GPU): so a grid that fills three quarters of the SMs' CTA slots is left alone. A
-    // smaller one is split so that the waves of CTAs, each as long as a segment's tiles, and the
-    // chain over the segments take the least time together: some 7.5 us a tile and 0.3 us a
-    // segment (measured: B8 D1536 L2048 0.98 ms in one sweep, 1.2 in 6 segments; B4 D1536 L2048
-    // 0.88 in one, 0.71 in 6; B1 D5120 L16384 6.0 in one, 3.35 in 9; d_state 128 with A per
-    // head, B2 D1536 L2048, 2.48 in one, 1.66 in 3).
+    // Segments: the number that the model above finds fastest. Segments fill SMs that one CTA per
+    // row and channel group leaves idle, or even out the last wave; they cost a second forward pass
+    // and the chain over them. Measured against 1 to 40 segments, 14 kernels at 8 shapes of over
+    // 80 us, the choice is 0.9 % off the best on average, at most 7 % (bf16 B8 D1536 L2048 N16:
+    // one sweep 0.89 ms, 1.07 in 3 segments; fp32 B4 D1536 L2048 N128: 6.98 in one, 5.97 in 3;
+    // bf16 B1 D3840 L8192 N16: 2.20 in one, 1.27 in 16).
     int64_t nseg = a->num_segments;
     if (nseg == 0) {
         const int64_t ctas = pl->groups * Bn, slots = (int64_t)kNumSMs * pl->v.ctas;
         nseg = 1;
-        if (ctas > 0 && 4 * ctas < 3 * slots) {
+        if (ctas > 0) {
             double best = 1e30;
-            const int64_t most = std::min<int64_t>({ntiles, 4 * slots / ctas, 1024});
-            for (int64_t n = 1; n <= most; ++n) {
-                const int64_t waves = (ctas * n + slots - 1) / slots, tiles = (ntiles + n - 1) / n;
-                const double t = waves * tiles * 7.5 * (n > 1 ? 1.1 : 1.0) + 0.3 * n;
+            const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8 * slots / ctas, 1024));
+            for (int64_t per = ntiles;; --per) {               // once for each number that differs
+                const int64_t n = (ntiles + per - 1) / per;
+                if (n > most) break;
+                per = (ntiles + n - 1) / n;
+                const double t = sweep_time(pl->v, pl->lanes, ctas, per, n);
                 if (t < best) {
                     best = t;
                     nseg = n;
                 }
+                if (per == 1) break;
             }
         }
     }

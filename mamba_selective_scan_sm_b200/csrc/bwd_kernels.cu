@@ -107,17 +107,27 @@ __global__ void __launch_bounds__(256) scan_bwd_reduce_heads_kernel(const BwdRed
     }
 }
 
-template <int S> static BwdVariant variant_of() {
-    using H = BwdShape<S>;
-    return {H::NS, H::G, H::TT, H::T, H::DRAIN, H::CTAS, H::KL - 1, H::NC - 1};
+template <int S, typename T, bool HEADS> static constexpr int ctas_of() {
+    constexpr int n = BwdSmem<T, S, false, false, HEADS>::CTAS;
+    static_assert(n == BwdSmem<T, S, true, false, HEADS>::CTAS && n == BwdSmem<T, S, false, true, HEADS>::CTAS &&
+                      n == BwdSmem<T, S, true, true, HEADS>::CTAS,
+                  "the workspace's size goes by neither the layout nor 8-bit inputs");
+    return n;
 }
-BwdVariant scan_bwd_variant(int lanes) {
-    return lanes == 1   ? variant_of<1>()
-           : lanes == 2 ? variant_of<2>()
-           : lanes == 4 ? variant_of<4>()
-           : lanes == 8 ? variant_of<8>()
-           : lanes == 16 ? variant_of<16>()
-                         : variant_of<32>();
+template <int S> static BwdVariant variant_of(int elem_size, bool heads) {
+    using H = BwdShape<S>;
+    using B = __nv_bfloat16;
+    const int ctas = elem_size == 2 ? (heads ? ctas_of<S, B, true>() : ctas_of<S, B, false>())
+                                    : (heads ? ctas_of<S, float, true>() : ctas_of<S, float, false>());
+    return {H::NS, H::G, H::TT, H::T, H::DRAIN, ctas, H::KL - 1, H::NC - 1};
+}
+BwdVariant scan_bwd_variant(int lanes, int elem_size, bool heads) {
+    return lanes == 1   ? variant_of<1>(elem_size, heads)
+           : lanes == 2 ? variant_of<2>(elem_size, heads)
+           : lanes == 4 ? variant_of<4>(elem_size, heads)
+           : lanes == 8 ? variant_of<8>(elem_size, heads)
+           : lanes == 16 ? variant_of<16>(elem_size, heads)
+                         : variant_of<32>(elem_size, heads);
 }
 
 cudaError_t launch_scan_bwd_carry(int ns, const BwdParams& p, cudaStream_t st) {

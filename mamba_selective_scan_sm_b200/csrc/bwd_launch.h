@@ -7,7 +7,8 @@
 
 namespace ssm {
 
-// Static shape of the backward scan kernels for `lanes` (1, 2, .. 32) lanes per channel.
+// Static shape of the backward scan kernels for `lanes` (1, 2, .. 32) lanes per channel; ctas
+// also goes by the activations' size and A per head (not by the layout or 8-bit inputs).
 struct BwdVariant {
     int ns, channels, tile;
     int steps;                    // between two checkpoints of the state
@@ -15,7 +16,7 @@ struct BwdVariant {
     int ctas;                     // of the backward sweep per SM
     int order_shift, order_mask;  // scratch states of channel d stand at n ^ (d >> shift & mask)
 };
-BwdVariant scan_bwd_variant(int lanes);
+BwdVariant scan_bwd_variant(int lanes, int elem_size, bool heads);
 
 // what: 0 checkpoints, 1 segment summaries, 2 the backward sweep. One per activation type,
 // layout (_cl: channel-last) and form of u, delta and z (_q8: int8 codes).

@@ -74,7 +74,7 @@ template <int S> struct BwdShape {
     static constexpr int W = S == 4 ? 2 : 4;                   // scan warps per CTA
     static constexpr int NH = S == 1 || S == 2 ? 128 : 64;     // helper threads
     static constexpr int NT = 32 * W + NH;
-    static constexpr int CTAS = S == 4 ? 3 : S >= 8 ? 2 : 1;   // per SM, by registers and shared memory
+    static constexpr int CTAS = S == 4 ? 3 : S >= 8 ? 2 : 1;   // per SM, by registers (see BwdSmem)
     static constexpr int KC = S <= 8 ? 1 : S / 8;              // such groups a warp takes in turn
     static constexpr int NC = CW < 4 ? CW : 4;                 // state orders (see slot_order)
     static constexpr int G = W * CW * KL * KC;                 // channels per CTA
@@ -473,6 +473,22 @@ template <typename T, int S, bool CL, bool Q8, bool ADJ> struct BwdCopies {
         id -= NY;
         return id < NB ? bc(p.Cm, p.sC, id, R::C) : none;
     }
+};
+
+// Shared memory of the sweep, and the CTAs that an SM holds with it: of fp32 d_state 9 to 16 (91 to
+// 101 KB) and of A per head there (77 to 81 KB in bf16) two instead of three, of fp32 d_state 65
+// to 128 (135 to 139 KB) one instead of two.
+template <typename T, int S, bool CL, bool Q8, bool HEADS> struct BwdSmem {
+    using H = BwdShape<S>;
+    static constexpr int kHead = (H::kPrm + H::kMask) * 4;
+    static constexpr int kRaw = BwdRaw<T, S, CL>::bytes(Q8);
+    static constexpr int kSweep =
+        (2 * H::kStaged(true, HEADS) + 6 * H::kOut + H::kPart + H::kCarry + (CL ? H::kSum : 0)) * 4 + kHead +
+        3 * kRaw + BwdCopies<T, S, CL, Q8, true>::COUNT * 16;
+    static constexpr int kPerSM = 228 * 1024, kReserved = 1024;   // an SM's, and of it the system's per CTA
+    static constexpr int kFit = kPerSM / (kSweep + kReserved);
+    static constexpr int CTAS = H::CTAS < kFit ? H::CTAS : kFit;
+    static_assert(CTAS >= 1, "a CTA fits an SM");
 };
 
 // The plain form of the same copies, element by element, for rows that are not aligned.
@@ -1098,7 +1114,8 @@ __global__ void __launch_bounds__(256) scan_bwd_carry_kernel(const BwdParams p) 
 
 // The backward sweep.
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
-__global__ void __launch_bounds__(BwdShape<S>::NT, BwdShape<S>::CTAS) scan_bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(BwdShape<S>::NT, BwdSmem<T, S, CL, Q8, HEADS>::CTAS)
+scan_bwd_kernel(const BwdParams p) {
     using H = BwdShape<S>;
     constexpr int KC = H::KC, KL = H::KL, ST = H::T, TT = H::TT, E = H::EPT;
     constexpr bool REGS = KC == 1;                             // m and dA in registers, else carried over

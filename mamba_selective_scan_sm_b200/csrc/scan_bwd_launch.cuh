@@ -20,7 +20,8 @@ inline cudaError_t launch_with_smem(K k, dim3 grid, int threads, int smem, const
 template <typename T, int S, bool CL, bool Q8, bool HEADS>
 inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t st) {
     using H = BwdShape<S>;
-    constexpr int kRaw = BwdRaw<T, S, CL>::bytes(Q8), kHead = (H::kPrm + H::kMask) * 4;
+    using M = BwdSmem<T, S, CL, Q8, HEADS>;
+    constexpr int kRaw = M::kRaw, kHead = M::kHead;
     const dim3 grid((p.dim + H::G - 1) / H::G, p.batch, p.nseg);
     if (what == 0)
         return launch_with_smem(scan_bwd_states_kernel<T, S, CL, Q8, HEADS, kCheckpoint>, grid, H::NT,
@@ -32,10 +33,7 @@ inline cudaError_t launch_scan_bwd_v(int what, const BwdParams& p, cudaStream_t 
                                 2 * H::kStaged(true, HEADS) * 4 + kHead + 2 * kRaw +
                                     BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
                                 p, st);
-    return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid, H::NT,
-                            (2 * H::kStaged(true, HEADS) + 6 * H::kOut + H::kPart + H::kCarry + (CL ? H::kSum : 0)) * 4 +
-                                kHead + 3 * kRaw + BwdCopies<T, S, CL, Q8, true>::COUNT * 16,
-                            p, st);
+    return launch_with_smem(scan_bwd_kernel<T, S, CL, Q8, HEADS>, grid, H::NT, M::kSweep, p, st);
 }
 
 template <typename T, bool CL, bool Q8>

@@ -112,10 +112,7 @@ __global__ void __launch_bounds__(kConvRowThreads, 6) conv_bwd_row_kernel(const 
 #pragma unroll
             for (int i = 0; i < R + 6; ++i) {
                 const int t = t0 - 3 + i;
-                float one[1] = {0.f};
-                if (t < 0) one[0] = conv_hist<T>(p, b, d, t);
-                else if (t < L) load_act<T, 1>(p.x, b, d, rev ? L - 1 - t : t, dir, true, 0, 1, one);
-                x[i] = one[0];
+                x[i] = t < 0 ? conv_hist<T>(p, b, d, t) : t < L ? load_act<T>(p.x, b, d, rev ? L - 1 - t : t) : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < R + 3; ++i) {

@@ -161,17 +161,16 @@ __device__ __forceinline__ void unpack4(uint32_t w, uint64_t (&v)[2]) {
                     __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443))), less);
 }
 
-// N codes of a run (a multiple of 4): whole and aligned in one access, else byte by byte.
+// N codes of a run (8 or 16): whole and aligned in one access, else byte by byte.
 template <int N>
 __device__ __forceinline__ void store_codes(int8_t* p, int hi, const uint32_t (&q)[N]) {
-    constexpr int V = N < 16 ? N : 16;
+    static_assert(N == 8 || N == 16, "one access");
     uint32_t w[N / 4];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = pack4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
-    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & (V - 1)) == 0) {
+    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & (N - 1)) == 0) {
         if constexpr (N == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(p) = w[0];
+        else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         return;
     }
 #pragma unroll
@@ -181,20 +180,18 @@ __device__ __forceinline__ void store_codes(int8_t* p, int hi, const uint32_t (&
 // The same codes as words of four; those past hi are 0.
 template <int N>
 __device__ __forceinline__ void load_code_words(const int8_t* p, int hi, uint32_t (&w)[N / 4]) {
-    constexpr int V = N < 16 ? N : 16;
-    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & (V - 1)) == 0) {
+    static_assert(N == 8 || N == 16, "one access");
+    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & (N - 1)) == 0) {
         if constexpr (N == 16) {
             const uint4 v = *reinterpret_cast<const uint4*>(p);
             w[0] = v.x;
             w[1] = v.y;
             w[2] = v.z;
             w[3] = v.w;
-        } else if constexpr (N == 8) {
+        } else {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
             w[0] = v.x;
             w[1] = v.y;
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
         }
         return;
     }
@@ -248,7 +245,7 @@ __global__ void __launch_bounds__(256) pack_row_kernel(const PackParams p) {
     const int t = in ? first * kBlock8 + (int)(idx % 8) * 8 : p.seqlen;
     const int hi = min(8, p.seqlen - t);
     float x[8];
-    load_run<T, 8>(static_cast<const T*>(p.x) + row * p.seqlen + t, 1, 0, hi, x);
+    load_run<T, 8>(static_cast<const T*>(p.x) + row * p.seqlen + t, hi, x);
     float top = max_mag(x);
 #pragma unroll
     for (int w = 1; w < 8; w *= 2) top = max_mag(top, top, __shfl_xor_sync(0xffffffffu, top, w));
@@ -333,7 +330,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const PackParams p) {
         divide(row, p.seqlen, b, t);
         const int blk = t / kBlock8;
         float s[8];
-        load_run<float, 8>(p.scales + (b * nb + blk) * p.dim + k, 1, 0, hi, s);
+        load_run<float, 8>(p.scales + (b * nb + blk) * p.dim + k, hi, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= s[i];
     } else {
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(256) unpack_kernel(const PackParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= s;
     }
-    store_run<T, 8>(static_cast<T*>(p.out) + row * inner + k, 1, 0, hi, f);
+    store_run<T, 8>(static_cast<T*>(p.out) + row * inner + k, hi, f);
 }
 
 // ----------------------------------------------------------------- decode states --
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const CacheParams p) {
         if (p.vec) {
             if (live) take_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, false, h[k]);
         } else {
-            load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, 1, 0, live ? n : 0, h[k]);
+            load_run<float, 8>(p.state + (int64_t)row * p.dstate + 8 * j, live ? n : 0, h[k]);
         }
     }
 #pragma unroll
@@ -426,7 +423,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheParams p) {
     const float s = p.scales[at];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] *= s;
-    store_run<T, 8>(static_cast<T*>(p.out) + (int64_t)brow * p.dstate + 8 * j, 1, 0, n, h);
+    store_run<T, 8>(static_cast<T*>(p.out) + (int64_t)brow * p.dstate + 8 * j, n, h);
 }
 
 // One decode step on the cache. A thread holds 16 states of a channel (LPR threads a
@@ -487,7 +484,7 @@ __global__ void __launch_bounds__(kUpdateThreads, kUpdateCtas) cached_update_ker
 #pragma unroll
             for (int i = 0; i < 16; ++i) A2[i] = a;
         } else {
-            load_run<float, 16>(p.A + d * p.dstate + 16 * j, 1, 0, n, A2);
+            load_run<float, 16>(p.A + d * p.dstate + 16 * j, n, A2);
 #pragma unroll
             for (int i = 0; i < 16; ++i) A2[i] *= kLog2e;
         }

@@ -146,93 +146,48 @@ template <typename T, int S, bool CL> struct BwdRaw {
     static constexpr int bytes(bool q8) { return SC + (q8 ? 6 * H::G * 4 : 0); }
 };
 
-// f[i] = element lo..hi-1 of a run (others 0) at p + i * step; one 16-byte (or two, or one
-// 8-byte) load when the run is dense, whole and aligned, in either direction.
+// The first hi of N dense elements from p on (others 0): 16-byte loads when all of them are there
+// and aligned.
 template <typename T, int N>
-__device__ __forceinline__ void load_run(const T* p, int64_t step, int lo, int hi, float (&f)[N]) {
+__device__ __forceinline__ void load_run(const T* p, int hi, float (&f)[N]) {
     constexpr int BY = N * (int)sizeof(T);
-    if constexpr (BY >= 8) {
-        constexpr int V = BY >= 16 ? 16 : 8;
-        const T* q = step < 0 ? p - (N - 1) : p;
-        if (lo <= 0 && hi >= N && (step == 1 || step == -1) &&
-            (reinterpret_cast<uintptr_t>(q) & (V - 1)) == 0) {
-            alignas(16) T e[N];
-            if constexpr (V == 16) {
+    static_assert(BY % 16 == 0, "runs of whole 16-byte units");
+    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        alignas(16) T e[N];
 #pragma unroll
-                for (int k = 0; k < BY / 16; ++k)
-                    reinterpret_cast<uint4*>(e)[k] = reinterpret_cast<const uint4*>(q)[k];
-            } else {
-                *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(q);
-            }
-            if (step > 0) {
+        for (int k = 0; k < BY / 16; ++k) reinterpret_cast<uint4*>(e)[k] = reinterpret_cast<const uint4*>(p)[k];
 #pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(e[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(e[N - 1 - i]);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        f[i] = i >= lo && i < hi ? Elem<T>::to_f(p[(int64_t)i * step]) : 0.f;
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void store_run(T* p, int64_t step, int lo, int hi, const float (&f)[N]) {
-    constexpr int BY = N * (int)sizeof(T);
-    if constexpr (BY >= 8) {
-        constexpr int V = BY >= 16 ? 16 : 8;
-        T* q = step < 0 ? p - (N - 1) : p;
-        if (lo <= 0 && hi >= N && (step == 1 || step == -1) &&
-            (reinterpret_cast<uintptr_t>(q) & (V - 1)) == 0) {
-            alignas(16) T e[N];
-            if (step > 0) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) e[i] = Elem<T>::from_f(f[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) e[N - 1 - i] = Elem<T>::from_f(f[i]);
-            }
-            if constexpr (V == 16) {
-#pragma unroll
-                for (int k = 0; k < BY / 16; ++k)
-                    reinterpret_cast<uint4*>(q)[k] = reinterpret_cast<uint4*>(e)[k];
-            } else {
-                *reinterpret_cast<uint2*>(q) = *reinterpret_cast<uint2*>(e);
-            }
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (i >= lo && i < hi) p[(int64_t)i * step] = Elem<T>::from_f(f[i]);
-}
-
-// A run of N elements of an activation, along positions (alongp: from channel c, position
-// pos, positions going by dir) or along channels (from channel c at position pos). Elements
-// lo..hi-1 exist; the others read 0.
-template <typename T, int N>
-__device__ __forceinline__ void load_act(const ActIn& a, int b, int c, int pos, int dir,
-                                         bool alongp, int lo, int hi, float (&f)[N]) {
-    const int64_t off = (int64_t)b * a.s.b + (int64_t)c * a.s.c + (int64_t)pos * a.s.p;
-    const int64_t step = alongp ? dir * a.s.p : a.s.c;
-    if (!a.scale) {
-        load_run<T, N>(static_cast<const T*>(a.p) + off, step, lo, hi, f);
+        for (int i = 0; i < N; ++i) f[i] = Elem<T>::to_f(e[i]);
         return;
     }
-    const int8_t* q = static_cast<const int8_t*>(a.p) + off;
-    const float* sc = a.scale + (int64_t)b * a.ss.b;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        f[i] = 0.f;
-        if (i >= lo && i < hi) {
-            const int pi = alongp ? pos + dir * i : pos, ci = alongp ? c : c + i;
-            f[i] = (float)q[(int64_t)i * step] *
-                   sc[(int64_t)ci * a.ss.c + (int64_t)(pi / kBlock8) * a.ss.p];
-        }
+    for (int i = 0; i < N; ++i) f[i] = i < hi ? Elem<T>::to_f(p[i]) : 0.f;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_run(T* p, int hi, const float (&f)[N]) {
+    constexpr int BY = N * (int)sizeof(T);
+    static_assert(BY % 16 == 0, "runs of whole 16-byte units");
+    if (hi >= N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        alignas(16) T e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = Elem<T>::from_f(f[i]);
+#pragma unroll
+        for (int k = 0; k < BY / 16; ++k) reinterpret_cast<uint4*>(p)[k] = reinterpret_cast<uint4*>(e)[k];
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < hi) p[i] = Elem<T>::from_f(f[i]);
+}
+
+// One element of an activation: channel c, position pos of batch row b.
+template <typename T>
+__device__ __forceinline__ float load_act(const ActIn& a, int b, int c, int pos) {
+    const int64_t off = (int64_t)b * a.s.b + (int64_t)c * a.s.c + (int64_t)pos * a.s.p;
+    if (!a.scale) return Elem<T>::to_f(static_cast<const T*>(a.p)[off]);
+    return (float)static_cast<const int8_t*>(a.p)[off] *
+           a.scale[(int64_t)b * a.ss.b + (int64_t)c * a.ss.c + (int64_t)(pos / kBlock8) * a.ss.p];
 }
 
 __device__ __forceinline__ float sigmoidf_(float v) {
@@ -613,7 +568,8 @@ __device__ __forceinline__ void take_run(const T* p, bool rev, float (&f)[N]) {
 // vec: such runs are aligned to their size.
 template <typename T, int N>
 __device__ __forceinline__ void put_run(T* p, bool rev, bool vec, int hi, const float (&f)[N]) {
-    constexpr int BY = N * (int)sizeof(T), V = BY >= 16 ? 16 : BY;
+    constexpr int BY = N * (int)sizeof(T), V = BY >= 16 ? 16 : 8;
+    static_assert(BY % V == 0, "whole units");
     if (vec && hi == N) {
         alignas(16) T e[N];
 #pragma unroll
@@ -621,8 +577,7 @@ __device__ __forceinline__ void put_run(T* p, bool rev, bool vec, int hi, const 
 #pragma unroll
         for (int k = 0; k < BY / V; ++k) {
             if constexpr (V == 16) reinterpret_cast<uint4*>(p)[k] = reinterpret_cast<uint4*>(e)[k];
-            else if constexpr (V == 8) reinterpret_cast<uint2*>(p)[k] = reinterpret_cast<uint2*>(e)[k];
-            else reinterpret_cast<uint32_t*>(p)[k] = reinterpret_cast<uint32_t*>(e)[k];
+            else reinterpret_cast<uint2*>(p)[k] = reinterpret_cast<uint2*>(e)[k];
         }
         return;
     }

@@ -787,10 +787,14 @@ __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_
 // Decay of one step for a lane's 4 states: 2^(delta A log2 e). d2: delta twice.
 // The SFU's exp comes out low on average: by 5e-9 to 8e-9 of its value for exponents above
 // -0.003, by 1.3e-8 to 2.9e-8 from there to -1 (means over 4 M random arguments each). A state
-// that decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which showed in
-// dA (2.5e-6 of its norm at the 130M layer's sizes, where an unbiased exp leaves 1.2e-6). The
-// exponent is therefore raised by the middle of that range, in the multiply that forms it.
-constexpr float kExpBias = 2.5e-8f;
+// that decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which shows in dA.
+// The exponent is therefore raised in the multiply that forms it, by what the slowest states
+// want, who collect it longest (1.2e-8 raises the value by 8.3e-9); the faster ones keep half of
+// theirs. Measured on dA against fp64 over 4000 steps, times 1e-7 of its norm, deltas of 2e-4 to
+// 1e-3 / 1e-3 to 0.01 / 0.01 to 0.1: 70 / 29 / 11; raised by 2.5e-8 296 / 104 / 5; not at all
+// (6000 steps) 169 / 63 / 15; torch's fp32 376 / 137 / 3. An exponent of 0 (delta = 0) still
+// gives 1 exactly: 8.3e-9 is far below half a step of it.
+constexpr float kExpBias = 1.2e-8f;
 __device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint64_t (&a)[2]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {

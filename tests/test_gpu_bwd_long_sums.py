@@ -65,3 +65,27 @@ def test_steps_without_time_change_no_bit(N, heads, segments, cl):
     assert torch.equal(out.dinitial_state, dhl)
     dC = t(out.dC)
     assert torch.equal(dC[:, :, 4000], h0[:, 7])
+
+
+@pytest.mark.parametrize("cl", [False, True])
+@pytest.mark.parametrize("segments", [1, 4])
+def test_slow_states_keep_their_memory(segments, cl):
+    """Decays of 2^x with x between -0.003 and 0, all terms of one sign. A state remembers 1 / (1 - a)
+    steps and takes up the decay's mean error e once for each: dA, a product of two such states, is off
+    by at most 2 e / (1 - a). The SFU's exp is low by 5e-9 to 8e-9 there and the kernel raises its
+    exponents by 1.2e-8, its values by 8.3e-9: e is at most 3.3e-9. The decays' own roundings are of
+    either sign, 2^-25 each at most: over 8192 steps 90 of them add up, 2.7e-6 (and lambda's as much)."""
+    from tests import bwd_reference as ref
+    m, (D, L, N) = ssm(), (6, 8192, 4)
+    r = np.random.default_rng(5)
+    delta = r.uniform(1e-4, 1e-3, (1, D, L)).astype(np.float32)
+    A = -np.linspace(0.5, 2.0, D * N).reshape(D, N).astype(np.float32)
+    u, dout = (r.uniform(0.5, 1.5, (1, D, L)).astype(np.float32) for _ in range(2))
+    B, C = (r.uniform(0.5, 1.5, (1, N, L)).astype(np.float32) for _ in range(2))
+    want = ref.scan_grads(dout, u, delta, A, B, C, softplus=False)["dA"]
+    t = lambda v: torch.from_numpy(v.transpose(0, 2, 1).copy() if cl else v).cuda()  # noqa: E731
+    g = m.ssm_selective_scan_bwd(t(dout), t(u), t(delta), torch.from_numpy(A).cuda(), t(B), t(C), delta_softplus=False,
+                                 channel_last=cl, num_segments=segments)
+    memory = 1.0 / (delta.mean() * -A.astype(np.float64))
+    off = np.abs(g.dA.cpu().numpy() / want - 1)
+    assert np.all(off <= 2 * 3.3e-9 * memory + 2 * 2.7e-6), off / memory

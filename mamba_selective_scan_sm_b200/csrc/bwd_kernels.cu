@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(256) since_kernel(const int32_t* cu, int nseq,
 // takes kReduceSteps steps of one batch row; the sums pass through shared memory, since
 // (batch, dstate, seqlen) outputs run along the steps and the partial rows along the states.
 constexpr int kReduceSteps = 8;
+constexpr int kReduceGroups = 64;  // whose sum is taken by itself: 2^20 channels make 32768 groups
 template <typename T>
 __global__ void __launch_bounds__(128) scan_bwd_reduce_bc_kernel(const BwdReduceParams p) {
     extern __shared__ float sm[];
@@ -36,13 +37,21 @@ __global__ void __launch_bounds__(128) scan_bwd_reduce_bc_kernel(const BwdReduce
     const float* src = p.parts + ((int64_t)b * p.seqlen + t0) * row;
     for (int k = threadIdx.x * 4; k < nt * row; k += blockDim.x * 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g0 = 0; g0 < p.groups; g0 += kReduceGroups) {  // in two steps: short chains
+            float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int g1 = min(p.groups, g0 + kReduceGroups);
 #pragma unroll 8
-        for (int g = 0; g < p.groups; ++g) {
-            const float4 q = *reinterpret_cast<const float4*>(src + g * gstride + k);
-            v.x += q.x;
-            v.y += q.y;
-            v.z += q.z;
-            v.w += q.w;
+            for (int g = g0; g < g1; ++g) {
+                const float4 q = *reinterpret_cast<const float4*>(src + g * gstride + k);
+                part.x += q.x;
+                part.y += q.y;
+                part.z += q.z;
+                part.w += q.w;
+            }
+            v.x += part.x;
+            v.y += part.y;
+            v.z += part.z;
+            v.w += part.w;
         }
         float* o = sm + (k / row) * (row + 1) + k % row;
         o[0] = v.x;

@@ -22,7 +22,7 @@ constexpr int kConvClChunk = 64;                               // steps per thre
 constexpr int kConvClRun = 4;                                  // channels per thread
 constexpr int kConvClAhead = 4;                                // steps whose loads are issued together
 
-// d silu(v) / dv
+// d silu(v) / dv (sigmoidf_ says how exactly)
 __device__ __forceinline__ float dsilu(float v) {
     const float s = sigmoidf_(v);
     return s * fmaf(v, 1.f - s, 1.f);

@@ -106,7 +106,9 @@ SSM_API const char* ssm_last_error_detail(void);
  *   x[b,d,s<0] = 0, act = SiLU if apply_silu else identity.
  * x, out: (batch, dim, seqlen) in dtype, device; w: (dim, width) fp32; bias: (dim)
  * fp32 or NULL. width in 1..4. batch, dim, seqlen >= 0 (zero sizes launch nothing).
- * out must not overlap x (SSM_ERR_ALIAS).
+ * out must not overlap x (SSM_ERR_ALIAS). A narrower conv is computed as one of 4 taps with
+ * zeros in front, here and fused in the scan: an infinity or a NaN in x then reaches the 3
+ * outputs behind it, not width - 1 (finite inputs are not affected).
  */
 SSM_API ssm_status_t ssm_causal_conv1d_fwd(const void* x, const float* w, const float* bias, void* out,
                                    int64_t batch, int64_t dim, int64_t seqlen, int32_t width,
@@ -305,7 +307,8 @@ SSM_API ssm_status_t ssm_selective_scan_fwd_noalloc(const ssm_scan_args_t* args,
  * these are the adjoints of the formulas above), and activations kept in 8 bits between
  * the two passes. Conventions as above: nothing is allocated, arguments are checked
  * before any launch, and the sums over batch, positions and channels are taken in fp32 in
- * a fixed order, so that a call repeated on the same inputs gives the same bits.
+ * a fixed order (those over long rows with what their additions round off beside them), so
+ * that a call repeated on the same inputs gives the same bits.
  * Calls that may run at the same time (other streams, graphs replayed side by side) need
  * a workspace each. */
 
@@ -377,12 +380,15 @@ SSM_API ssm_status_t ssm_selective_scan_bwd_workspace_size(const ssm_scan_bwd_ar
 
 /*
  * Gradients of ssm_selective_scan_fwd with respect to all its inputs, from those inputs
- * alone (nothing of the forward call is kept but them). Covers what the forward call
- * covers with input-dependent B and C in one direction: either layout, the fused conv,
- * the reverse direction, a continued sequence, packed sequences, A per head, d_state up
- * to 128. The gradient of the bidirectional sum is the sum of two calls, one per
- * direction. No output may overlap an input or another output, element for element
- * (views of one tensor, such as du and dz in the halves of an in_proj gradient, are fine).
+ * alone (nothing of the forward call is kept but them). Covers the forward call in one
+ * direction with input-dependent B and C: either layout, the fused conv, the reverse
+ * direction, a continued sequence, packed sequences (but for the gradient of their final
+ * states), A per head, d_state up to 128. The gradient of the bidirectional sum is the sum
+ * of two calls, one per direction; time-invariant B and C have none. No output may share an
+ * element with an input or another output: views of one tensor side by side, with the same
+ * position stride, are fine (du and dz in the halves of an in_proj gradient, or in free
+ * columns beside u and z). With a conv of fewer than 4 taps what is not finite reaches as far
+ * as those taps.
  * Errors: as the forward call's; SSM_ERR_UNSUPPORTED also for dfinal_state with
  * seq_starts, and for initial_state, conv_history, dinitial_state with reverse;
  * SSM_ERR_NULL_ARG for an output whose input is missing, and for u_scale without

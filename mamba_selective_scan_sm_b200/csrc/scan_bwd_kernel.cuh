@@ -31,7 +31,7 @@
 // scan_bwd_reduce_bc_kernel from one partial row per CTA: no atomics, so the sums come out in
 // the same order every time.
 //
-// What bounds it (B8 D1536 L2048 N16 bf16 + conv: 0.25 ms checkpoints, 0.65 ms sweep): latency.
+// What bounds it (B8 D1536 L2048 N16 bf16 + conv: 0.25 ms checkpoints, 0.66 ms sweep): latency.
 // 384 CTAs give an SM five scan warps, which issue 0.25 instructions a cycle each through
 // dependent exps, multiplies and shuffles; issue slots 46 % busy, shared memory 58 %, DRAM
 // 17 %. Measured otherwise, sweep alone: every warp both staging and scanning one channel per
@@ -775,47 +775,55 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
     }
 }
 
-// A of one lane's 4 states (times log2 e), zeros past dim or d_state.
+// A of one lane's 4 states (times log2 e). Past dim or d_state stands a large one, which is never a
+// lane's smallest (see decays); those states hold zeros, and past dim delta is 0 as well.
+constexpr float kNoState = -1e4f;
 template <int S>
 __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_t (&A2)[2]) {
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int n = 4 * j + (k ^ slot_order<S>(d));
-        a[k] = d < p.dim && n < p.dstate ? kLog2e * p.A[(int64_t)d * p.dstate + n] : 0.f;
+        a[k] = d < p.dim && n < p.dstate ? kLog2e * p.A[(int64_t)d * p.dstate + n] : kNoState;
     }
     A2[0] = pk2(a[0], a[1]);
     A2[1] = pk2(a[2], a[3]);
 }
 
-// Decay of one step for a lane's 4 states: 2^(delta A log2 e). d2: delta twice.
-// The SFU's exp comes out low on average: by 5e-9 to 8e-9 of its value for exponents above
-// -0.003, by 1.3e-8 to 2.9e-8 from there to -1 (means over 4 M random arguments each). A state
-// that decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which shows in dA.
-// The exponent is therefore raised in the multiply that forms it, by what the slowest states
-// want, who collect it longest (1.2e-8 raises the value by 8.3e-9); the faster ones keep half of
-// theirs. Measured on dA against fp64 over 4000 steps, times 1e-7 of its norm, deltas of 2e-4 to
-// 1e-3 / 1e-3 to 0.01 / 0.01 to 0.1: 70 / 29 / 11; raised by 2.5e-8 296 / 104 / 5; not at all
-// (6000 steps) 169 / 63 / 15; torch's fp32 376 / 137 / 3. An exponent of 0 (delta = 0) still
-// gives 1 exactly: 8.3e-9 is far below half a step of it.
-constexpr float kExpBias = 1.2e-8f;
-__device__ __forceinline__ void decay(const uint64_t (&A2)[2], uint64_t d2, uint64_t (&a)[2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float2 x = upk2(fma2(d2, A2[k], pk2(kExpBias, kExpBias)));
-        a[k] = pk2(ex2(x.x), ex2(x.y));
-    }
-}
-
-// Decays and delta u of the T steps from row. With A per head the decays are staged (from as).
+// Decays of T steps for a lane's 4 states, 2^(delta A log2 e), and the steps' delta u, from row.
+// With A per head the decays are staged (from as).
+// The SFU's exp comes out low on average: by 6e-9 of its value for exponents above -0.004, by 2e-8
+// to 3e-8 from there to -1 (means over 0.5 M random arguments in each of 46 ranges). A state that
+// decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which shows in dA. The
+// exponent is therefore raised by that (over ln 2), in the multiply that forms it: by the one or the
+// other for all T steps, as the first step's delta and the lane's smallest A say (0.7 % of the
+// call's time). dA against fp64 over 4000 steps, in 1e-7 of its norm, at deltas of 2e-4 to 1e-3 /
+// 1e-3 to 0.01 / 0.01 to 0.1: 22 / 12 / 4; torch's fp32 376 / 137 / 3; one raise for all, by 2.5e-8,
+// 296 / 104 / 5, by 1.2e-8 70 / 29 / 11. An exponent of 0 (delta = 0) still gives 1 exactly: 6e-9 is
+// far below half a step of it.
+constexpr float kExpBiasSlow = 0.9e-8f, kExpBiasFast = 3.1e-8f, kSlow = 0.004f;
 template <bool HEADS, int T>
 __device__ __forceinline__ void decays(const uint64_t (&A2)[2], const float2* row, const float* as,
                                        uint64_t (&a)[T][2], uint64_t (&du2)[T]) {
+    uint64_t raise = 0;
+    if constexpr (!HEADS) {
+        const float2 x = upk2(A2[0]), y = upk2(A2[1]);
+        const float least = fminf(fminf(fabsf(x.x), fabsf(x.y)), fminf(fabsf(y.x), fabsf(y.y)));
+        const float r = row[0].x * least < kSlow ? kExpBiasSlow : kExpBiasFast;
+        raise = pk2(r, r);
+    }
 #pragma unroll
     for (int i = 0; i < T; ++i) {
         const float2 s = row[i];
-        if constexpr (HEADS) a[i][0] = a[i][1] = pk2(as[i], as[i]);
-        else decay(A2, pk2(s.x, s.x), a[i]);
+        if constexpr (HEADS) {
+            a[i][0] = a[i][1] = pk2(as[i], as[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 e = upk2(fma2(pk2(s.x, s.x), A2[k], raise));
+                a[i][k] = pk2(ex2(e.x), ex2(e.y));
+            }
+        }
         du2[i] = pk2(s.y, s.y);
     }
 }

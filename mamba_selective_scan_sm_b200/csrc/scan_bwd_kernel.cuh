@@ -31,9 +31,9 @@
 // scan_bwd_reduce_bc_kernel from one partial row per CTA: no atomics, so the sums come out in
 // the same order every time.
 //
-// What bounds it (B8 D1536 L2048 N16 bf16 + conv: 0.25 ms checkpoints, 0.66 ms sweep): latency.
+// What bounds it (B8 D1536 L2048 N16 bf16 + conv: 0.26 ms checkpoints, 0.65 ms sweep): latency.
 // 384 CTAs give an SM five scan warps, which issue 0.25 instructions a cycle each through
-// dependent exps, multiplies and shuffles; issue slots 46 % busy, shared memory 58 %, DRAM
+// dependent exps, multiplies and shuffles; issue slots 48 % busy, shared memory 60 %, DRAM
 // 17 %. Measured otherwise, sweep alone: every warp both staging and scanning one channel per
 // lane 0.79 ms, two channels per lane 0.92 (fewer instructions, half the warps); tiles of 8
 // steps 0.69; two sub-tiles in hand per scan warp 1.10 (spills).

@@ -775,16 +775,16 @@ __device__ __forceinline__ void stage_tile(const BwdParams& p, int hid, int b, i
     }
 }
 
-// A of one lane's 4 states (times log2 e). Past dim or d_state stands a large one, which is never a
-// lane's smallest (see decays); those states hold zeros, and past dim delta is 0 as well.
-constexpr float kNoState = -1e4f;
+// A of one lane's 4 states (times log2 e), zeros past dim. Past d_state stands the last state's:
+// those states hold zeros and keep them, as long as that state's decay is finite (a negative delta
+// makes it grow), and the lane's smallest A is one of the channel's (see decays).
 template <int S>
 __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_t (&A2)[2]) {
     float a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int n = 4 * j + (k ^ slot_order<S>(d));
-        a[k] = d < p.dim && n < p.dstate ? kLog2e * p.A[(int64_t)d * p.dstate + n] : kNoState;
+        a[k] = d < p.dim ? kLog2e * p.A[(int64_t)d * p.dstate + min(n, p.dstate - 1)] : 0.f;
     }
     A2[0] = pk2(a[0], a[1]);
     A2[1] = pk2(a[2], a[3]);

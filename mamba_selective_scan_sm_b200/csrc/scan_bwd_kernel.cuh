@@ -796,7 +796,7 @@ __device__ __forceinline__ void load_A(const BwdParams& p, int d, int j, uint64_
 // to 3e-8 from there to -1 (means over 0.5 M random arguments in each of 46 ranges). A state that
 // decays by 1 - a per step collects such a bias over 1 / (1 - a) steps, which shows in dA. The
 // exponent is therefore raised by that (over ln 2), in the multiply that forms it: by the one or the
-// other for all T steps, as the first step's delta and the lane's smallest A say (0.7 % of the
+// other for all T steps, as the first step's delta and the lane's smallest A say (1 % of the
 // call's time). dA against fp64 over 4000 steps, in 1e-7 of its norm, at deltas of 2e-4 to 1e-3 /
 // 1e-3 to 0.01 / 0.01 to 0.1: 22 / 12 / 4; torch's fp32 376 / 137 / 3; one raise for all, by 2.5e-8,
 // 296 / 104 / 5, by 1.2e-8 70 / 29 / 11. An exponent of 0 (delta = 0) still gives 1 exactly: 6e-9 is

@@ -123,3 +123,57 @@ def test_steps_repeat_their_bits():
     first = tokens()
     for _ in range(3):
         assert all(torch.equal(p, q) for p, q in zip(first, tokens()))
+
+
+@pytest.mark.parametrize("random", [False, True])
+def test_the_step_over_all_magnitudes(random):
+    """Rows of every code at scales 2^k, the largest state from 2^-99 to 2^127: quotients are whole
+    numbers, so every code stays (at random but for 3e-7 of them: none of 29,000 to expect). Below
+    2^-100 a row becomes zeros."""
+    m, n = ssm(), 128
+    k = torch.arange(-112, 121, device="cuda")
+    dim = len(k)
+    row = torch.cat([torch.arange(0, 128, 2), -torch.arange(1, 129, 2)]).to(torch.int8)
+    codes = row.cuda().repeat(1, dim, 1)
+    scales = torch.exp2(k.double()).float()[None].contiguous()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    zero, bc = torch.zeros(1, dim, device="cuda"), torch.zeros(1, n, device="cuda")
+    want, ws = codes.clone(), scales.clone()
+    top = codes.abs().amax(-1).float() * scales
+    want[top < 2.0 ** -100], ws[top < 2.0 ** -100] = 0, 0
+    for _ in range(2):
+        rand = torch.randint(-2 ** 31, 2 ** 31, (1, dim), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+        m.ssm_selective_state_update_cached(codes, scales, None, zero, zero, torch.zeros(dim, n, device="cuda"), bc, bc,
+                                            dt_softplus=False, rand=rand if random else None)
+        assert torch.equal(codes, want) and torch.equal(scales, ws)
+
+
+@pytest.mark.parametrize("random", [False, True])
+@pytest.mark.parametrize("n", [3, 16, 64, 100])
+def test_a_step_that_is_not_finite(n, random):
+    """An infinity or a NaN in a channel's input makes that row of the slot read back as NaN, now and
+    after the next token; every other row keeps its bits."""
+    m, B, D = ssm(), 3, 40
+    g = torch.Generator(device="cuda").manual_seed(7)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    state, A, x, dt, Bt, Ct = r(B, D, n), -r(D, n).abs() - 0.1, r(B, D), r(B, D), r(B, n), r(B, n)
+    rand = torch.randint(-2 ** 31, 2 ** 31, (B, D), generator=g, device="cuda", dtype=torch.int64).to(torch.int32)
+    bad = [(0, 3, float("inf")), (1, 0, float("nan")), (2, 39, float("-inf"))]
+
+    def tokens(spoil):
+        codes, scales = torch.zeros(B, D, n, dtype=torch.int8, device="cuda"), torch.zeros(B, D, device="cuda")
+        m.ssm_state_cache_write(state, codes, scales)
+        first = x.clone()
+        for b, d, v in bad if spoil else []:
+            first[b, d] = v
+        y = [m.ssm_selective_state_update_cached(codes, scales, None, u, dt, A, Bt, Ct, rand=rand if random else None)
+             for u in (first, x)]
+        return [*y, m.ssm_state_cache_read(codes, scales)]
+    want, got = tokens(False), tokens(True)
+    keep = torch.ones(B, D, dtype=torch.bool, device="cuda")
+    for b, d, _ in bad:
+        keep[b, d] = False
+    for a, o in zip(got, want):
+        assert torch.equal(a[keep], o[keep])
+    assert torch.isnan(got[2][~keep]).all() and torch.isnan(got[1][~keep]).all()
+    assert not torch.isfinite(got[0][~keep]).any()

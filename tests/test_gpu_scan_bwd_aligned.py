@@ -87,6 +87,14 @@ def test_a_row_of_several_chunks(dtype, cl, reverse):
     run(case(38, dtype, 1, 48, 2080, 16, conv=4), dtype, cl, reverse=reverse, num_segments=1)
 
 
+@both
+@layouts
+@pytest.mark.parametrize("B,D,L,N", [(1, 640, 96, 16), (2, 1040, 32, 8), (1, 416, 64, 64)])
+def test_many_channels(dtype, cl, B, D, L, N):
+    """More channels than a CTA holds many times over: their sums meet outside it."""
+    run(case(39, dtype, B, D, L, N, conv=4), dtype, cl)
+
+
 # ------------------------------------------------------------- 8-bit activations --
 
 def from_8_bits(c, dtype, cl, reverse=False, starts=None, **kw):
